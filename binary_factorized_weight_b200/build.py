@@ -22,8 +22,9 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libdbf.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
-SOURCES = ["dbf_api.cu", "decode.cu", "fused.cu", "prefill.cu", "pack.cu", "transpose.cu", "reconstruct.cu", "bqq.cu", "factorize.cu", "noalloc.cu"]
-HEADERS = ["dbf_device.cuh", "dbf_internal.h"]
+SOURCES = ["dbf_api.cu", "decode.cu", "fused.cu", "prefill.cu", "pack.cu", "transpose.cu", "reconstruct.cu", "bqq.cu", "factorize.cu", "noalloc.cu",
+           "mx_quantize.cu", "mx_forward.cu", "rmsnorm.cu"]
+HEADERS = ["dbf_device.cuh", "mx_device.cuh", "dbf_internal.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

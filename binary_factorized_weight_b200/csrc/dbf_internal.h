@@ -2,6 +2,8 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -138,6 +140,9 @@ dbf_status launch_reconstruct(const uint32_t* packedA, const uint32_t* packedB, 
                               const __half* b, int64_t n, int64_t k, int64_t m_in, void* W, bool out_f32,
                               const DeviceInfo& dev, cudaStream_t stream);
 
+// cuTensorMapEncodeTiled through the runtime's driver entry point (null if unavailable).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
 inline int64_t words_per_row(int64_t cols) { return cols <= 0 ? 0 : ((cols + 255) / 256) * 8; }
 
 // Plain launch that reports this launch's own error (not a pending one).
@@ -152,5 +157,37 @@ inline dbf_status launch_plain(void (*kernel)(KArgs...), dim3 grid, dim3 block, 
   cfg.numAttrs = 0;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...) == cudaSuccess ? DBF_OK : DBF_ERR_CUDA;
 }
+
+// Launch with programmatic stream serialization: the kernel may be scheduled
+// once its predecessor on the stream has triggered, and waits for it itself
+// (griddepcontrol.wait) before it touches memory.
+template <typename... KArgs, typename... Args>
+inline dbf_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                             Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...) == cudaSuccess ? DBF_OK : DBF_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- MX operands and dense rows
+constexpr int64_t kMaxMxCols = int64_t{1} << 24;  // rows and columns of an MX matrix or a dense row matrix
+
+inline bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+inline int64_t mx_pitch(int64_t cols) { return (cols + 127) / 128 * 128; }
+// rows, cols in [1, 1 << 24] and at most 2^40 elements (every offset fits 64 bits, a byte pitch 32).
+inline bool mx_shape_ok(int64_t rows, int64_t cols) {
+  return rows >= 1 && cols >= 1 && rows <= kMaxMxCols && cols <= kMaxMxCols && rows * mx_pitch(cols) <= (int64_t{1} << 40);
+}
+inline bool mx_format_ok(int fmt) { return fmt == DBF_MX_E2M1 || fmt == DBF_MX_E4M3; }
+inline bool float_dtype_ok(int t) { return t == DBF_F16 || t == DBF_F32 || t == DBF_BF16; }
+inline size_t dtype_size(int t) { return t == DBF_F32 ? 4 : 2; }
 
 }  // namespace dbf

@@ -1,0 +1,453 @@
+// Product of two microscaled matrices on the fifth-generation tensor cores:
+//
+//   y[t][i] = sum_k 2^(ex[t][k] + ew[i][k]) sum_{j < 32} qx[t][32k + j] qw[i][32k + j]
+//
+// tcgen05 block-scaled MMA reads the codes as they are (two operands in 4 bits:
+// kind::mxf4, K 64 an instruction; else kind::mxf8f6f4, K 32, 4-bit rows being
+// widened to a byte per element by the TMA copy) and applies the scales of both
+// operands itself, from tensor memory.  Sums are fp32.
+//
+// A tile is 128 rows of one operand (P, the tensor cores' M) by NT of the other
+// (Q, their N).  A stage of the shared-memory ring is 128 bytes of every row:
+// 256 4-bit or 128 byte-wide elements of K, with the 512-byte scale tiles (128
+// rows x 128 elements) that belong to them.
+//
+// Roles (192 threads): warp 0 TMA producer; warp 1 tensor memory and the
+// single-thread issue of scale copies and MMAs; warps 2-5 epilogue.
+//
+// Few tiles (WROWS: P = the weight's rows, Q = the tokens, NT small): the K range
+// of a tile is split over a cluster, each CTA sends its fp32 partial of token t
+// to CTA t % size, which adds them in rank order.
+//
+// Every wait is bounded; one that gives up records DBF_ERR_TIMEOUT in the
+// workspace's status word and the kernel ends with y incomplete.
+#include <algorithm>
+#include <mutex>
+
+#include "dbf_internal.h"
+#include "mx_device.cuh"
+
+namespace dbf {
+namespace {
+
+constexpr int kRows = 128;  // rows of P per tile (TMEM lanes)
+constexpr int kThreads = 192;
+constexpr int kRowBytes = 128;  // bytes of a row per stage
+constexpr int kTileBytes = 512;  // a scale tile
+constexpr size_t kStatusBytes = 256;
+
+struct MxArgs {
+  const uint8_t* p_scales;
+  const uint8_t* q_scales;
+  int64_t p_rows, q_rows;
+  int64_t k4s;       // 128-element groups of K (scale tiles in a row of tiles)
+  int stages_k;      // stages of the whole K range
+  int p_tx, q_tx;    // bytes that a row of P, Q counts on its barrier
+  uint32_t idesc;
+  int p_static;      // P (WROWS) or Q holds weights that may be read before the PDL wait
+  void* out;
+  int64_t ld_out;
+  int out_t;
+  int* status;
+};
+
+template <int KA, int NT, bool WROWS>
+struct Cfg {
+  static constexpr int kQTiles = (NT + 127) / 128;  // scale tiles of Q's rows
+  static constexpr int kPBytes = kRows * kRowBytes;
+  static constexpr int kQBytes = NT * kRowBytes;
+  static constexpr int kScaleBytes = KA * (1 + kQTiles) * kTileBytes;
+  static constexpr int kStageBytes = kPBytes + kQBytes + kScaleBytes;
+  // the epilogue's area: the partial sums of a split tile, or the four warps'
+  // 32 x 33 transposes
+  static constexpr int kEpiBytes = WROWS ? NT * kRows * 4 : 4 * 32 * 33 * 4;
+  static constexpr int kRoom = 227 * 1024 - 1024 - 512 - kEpiBytes;
+  static constexpr int kStages = kRoom / kStageBytes < 8 ? kRoom / kStageBytes : 8;
+  static constexpr int kEpiOffset = kStages * kStageBytes;
+  static constexpr int kBarOffset = kEpiOffset + kEpiBytes;
+  static constexpr int kSmemBytes = kBarOffset + 512 + 1024;
+  static constexpr int kScaleCols = KA * 4 * (1 + kQTiles);
+  static constexpr int kDCols = NT < 32 ? 32 : NT;
+  static constexpr int kNeedCols = kDCols + kStages * kScaleCols;
+  static constexpr int kTmemCols = kNeedCols <= 128 ? 128 : kNeedCols <= 256 ? 256 : 512;
+  static_assert(kNeedCols <= 512, "accumulator and scales must fit in tensor memory");
+  static_assert(kStages >= 2, "");
+};
+
+__device__ __forceinline__ void store_out(void* out, int t, int64_t at, float v) {
+  if (t == DBF_F32) {
+    static_cast<float*>(out)[at] = v;
+  } else if (t == DBF_F16) {
+    static_cast<__half*>(out)[at] = __float2half_rn(v);
+  } else {
+    static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
+  }
+}
+
+template <int KA, int NT, bool WROWS>
+__global__ void __launch_bounds__(kThreads, 1)
+    dbf_mx_gemm_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
+                       const MxArgs a) {
+  using C = Cfg<KA, NT, WROWS>;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // operand rings first: their 128-byte swizzle counts from 1024-byte boundaries
+  uint8_t* p_st = smem;
+  uint8_t* q_st = smem + S * C::kPBytes;
+  uint8_t* s_st = q_st + S * C::kQBytes;
+  float* epi = reinterpret_cast<float*>(smem + C::kEpiOffset);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
+  uint64_t* empty = full + S;
+  uint64_t* acc_full = empty + S;
+  uint64_t* mma_done = acc_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ks = WROWS ? static_cast<int>(cluster_size()) : 1;
+  const int rank = WROWS ? static_cast<int>(cluster_rank()) : 0;
+  const int64_t p_tiles = (a.p_rows + kRows - 1) / kRows;
+  const int64_t tile = blockIdx.x / ks;
+  const int64_t p0 = (tile % p_tiles) * kRows, q0 = (tile / p_tiles) * NT;
+  const int kt0 = static_cast<int>(static_cast<int64_t>(a.stages_k) * rank / ks);
+  const int kt1 = static_cast<int>(static_cast<int64_t>(a.stages_k) * (rank + 1) / ks);
+
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tmap(&p_map);
+    prefetch_tmap(&q_map);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_launch_dependents();
+  // a rank's partial sums are written only after every CTA of its cluster has started
+  if constexpr (WROWS) cluster_arrive_relaxed();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------ TMA producer
+    if (lane == 0) {
+      // scale tiles of Q's rows that exist (the last tile of rows may stand alone)
+      const int q_tiles = static_cast<int>(min(static_cast<int64_t>(C::kQTiles), (a.q_rows - q0 + 127) >> 7));
+      auto load_p = [&](int kt, int s) {
+        const int atoms = static_cast<int>(min(static_cast<int64_t>(KA), a.k4s - static_cast<int64_t>(kt) * KA));
+        tma_load_2d(p_st + s * C::kPBytes, &p_map, kt * 128, static_cast<int>(p0), &full[s]);
+        bulk_load(s_st + s * C::kScaleBytes, a.p_scales + ((p0 >> 7) * a.k4s + static_cast<int64_t>(kt) * KA) * kTileBytes,
+                  atoms * kTileBytes, &full[s]);
+      };
+      auto load_q = [&](int kt, int s) {
+        const int atoms = static_cast<int>(min(static_cast<int64_t>(KA), a.k4s - static_cast<int64_t>(kt) * KA));
+        tma_load_2d(q_st + s * C::kQBytes, &q_map, kt * 128, static_cast<int>(q0), &full[s]);
+        for (int j = 0; j < q_tiles; ++j)
+          bulk_load(s_st + s * C::kScaleBytes + KA * (1 + j) * kTileBytes,
+                    a.q_scales + (((q0 >> 7) + j) * a.k4s + static_cast<int64_t>(kt) * KA) * kTileBytes,
+                    atoms * kTileBytes, &full[s]);
+      };
+      auto expect = [&](int kt, int s) {
+        const int atoms = static_cast<int>(min(static_cast<int64_t>(KA), a.k4s - static_cast<int64_t>(kt) * KA));
+        mbar_arrive_expect_tx(&full[s], kRows * a.p_tx + NT * a.q_tx + (1 + q_tiles) * atoms * kTileBytes);
+      };
+      // the first ring's worth of the weights is on its way before the wait for
+      // the kernel that writes the tokens
+      const int early = min(S, kt1 - kt0);
+      if (!a.p_static) pdl_wait();
+      for (int i = 0; i < early; ++i) {
+        expect(kt0 + i, i);
+        if (WROWS) load_p(kt0 + i, i);
+        else load_q(kt0 + i, i);
+      }
+      if (a.p_static) pdl_wait();
+      for (int i = 0; i < early; ++i) {
+        if (WROWS) load_q(kt0 + i, i);
+        else load_p(kt0 + i, i);
+      }
+      int it = early;
+      for (; kt0 + it < kt1; ++it) {
+        const int s = it % S;
+        if (!mbar_wait_bounded(&empty[s], (it / S - 1) & 1, abort_flag, a.status)) break;
+        expect(kt0 + it, s);
+        load_p(kt0 + it, s);
+        load_q(kt0 + it, s);
+      }
+      // after a wait that gave up: no copy may still be on its way when the CTA ends
+      if (*abort_flag) {
+        int never = 0;
+        for (int i = max(0, it - S); i < it; ++i) (void)mbar_wait_bounded(&full[i % S], (i / S) & 1, &never, a.status);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------ scale copies and MMAs
+    if (lane == 0) {
+      bool ok = true;
+      for (int kt = kt0, it = 0; kt < kt1; ++kt, ++it) {
+        const int s = it % S;
+        if (!mbar_wait_bounded(&full[s], (it / S) & 1, abort_flag, a.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sc = smem_u32(s_st + s * C::kScaleBytes);
+        const uint32_t sf = tmem + C::kDCols + s * C::kScaleCols;  // P's, then Q's columns
+#pragma unroll
+        for (int k = 0; k < KA; ++k) {
+          tc_copy_scales(sf + 4 * k, smem_desc_rows16(sc + k * kTileBytes));
+#pragma unroll
+          for (int j = 0; j < C::kQTiles; ++j)
+            tc_copy_scales(sf + 4 * KA + 4 * (k * C::kQTiles + j),
+                           smem_desc_rows16(sc + (KA * (1 + j) + k) * kTileBytes));
+        }
+        const uint32_t pa = smem_u32(p_st + s * C::kPBytes), qa = smem_u32(q_st + s * C::kQBytes);
+        // K behind the last group of 128 is not multiplied: its scales were not copied
+        const bool whole = KA == 1 || a.k4s - static_cast<int64_t>(kt) * KA >= KA;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          if (KA == 2 && kk >= 2 && !whole) break;
+          const uint32_t acc = it != 0 || kk != 0 ? 1u : 0u;
+          const uint64_t pd = smem_desc_sw128_kmajor(pa + kk * 32), qd = smem_desc_sw128_kmajor(qa + kk * 32);
+          if constexpr (KA == 2) {
+            const uint32_t id = 2u * (kk & 1);
+            tc_mma_mxf4(tmem, pd, qd, a.idesc | (id << 4) | (id << 29), sf + 4 * (kk >> 1),
+                        sf + 4 * KA + 4 * C::kQTiles * (kk >> 1), acc);
+          } else {
+            tc_mma_mxf8f6f4(tmem, pd, qd, a.idesc | (static_cast<uint32_t>(kk) << 4) | (static_cast<uint32_t>(kk) << 29),
+                            sf, sf + 4, acc);
+          }
+        }
+        tc_commit(&empty[s]);
+      }
+      if (ok) tc_commit(acc_full);
+      tc_commit(mma_done);
+    }
+  } else {
+    // ------------------------------------------------ epilogue
+    const int q = warp & 3;  // the TMEM lanes this warp may read
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_full, 0, abort_flag, a.status));
+    tc_fence_after();
+    const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    const int64_t p_row = p0 + q * 32 + lane;
+    if constexpr (WROWS) {
+      const int tokens = static_cast<int>(min(static_cast<int64_t>(NT), a.q_rows - q0));
+      if (ks == 1) {
+        for (int c = 0; c < tokens && ok; c += 16) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(acc + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c + j < tokens && p_row < a.p_rows)
+              store_out(a.out, a.out_t, (q0 + c + j) * a.ld_out + p_row, __uint_as_float(v[j]));
+        }
+      } else {
+        const int per = (tokens + ks - 1) / ks;  // tokens of a rank, at most
+        cluster_wait_acquire();
+        for (int c = 0; c < tokens && ok; c += 16) {
+          uint32_t v[16];
+          tmem_ld_32x32b_x16(acc + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int t = c + j;
+            if (t < tokens)
+              st_cluster_f32(map_to_rank(epi + (rank * per + t / ks) * kRows + q * 32 + lane, t % ks),
+                             __uint_as_float(v[j]));
+          }
+        }
+        cluster_arrive_release();
+        cluster_wait_acquire();
+        for (int t = rank; t < tokens && ok; t += ks) {
+          float sum = 0.f;
+          for (int src = 0; src < ks; ++src) sum += epi[(src * per + t / ks) * kRows + q * 32 + lane];
+          if (p_row < a.p_rows) store_out(a.out, a.out_t, (q0 + t) * a.ld_out + p_row, sum);
+        }
+      }
+    } else {
+      float* st = epi + q * 32 * 33;
+      const int64_t row0 = p0 + q * 32;
+      const int rows = static_cast<int>(max(int64_t{0}, min(int64_t{32}, a.p_rows - row0)));
+      for (int c = 0; c < NT && ok; c += 32) {
+        if (q0 + c >= a.q_rows) break;
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(acc + c, v);
+        tmem_ld_wait();
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) st[lane * 33 + j] = __uint_as_float(v[j]);
+        __syncwarp();
+        const int64_t col = q0 + c + lane;
+        if (col < a.q_rows)
+          for (int r = 0; r < rows; ++r) store_out(a.out, a.out_t, (row0 + r) * a.ld_out + col, st[r * 33 + lane]);
+      }
+    }
+  }
+
+  // ------------------------------------------------ teardown
+  if constexpr (WROWS) {
+    // every thread takes part in the cluster's barriers: the epilogue's two of a
+    // split tile, or one to pair the first arrival
+    __syncwarp();
+    if (ks == 1) {
+      cluster_wait_acquire();
+    } else if (warp < 2) {
+      cluster_wait_acquire();
+      cluster_arrive_release();
+      cluster_wait_acquire();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    (void)mbar_wait_bounded(mma_done, 0, abort_flag, a.status);
+    __syncwarp();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------- host
+struct Operand {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t rows;
+  bool four;  // 4-bit codes
+};
+
+// The map of one operand's codes: 128-byte rows of the ring.  mxf4 copies the
+// packed bytes; mxf8f6f4 copies bytes, or widens 16 4-bit elements to 16 bytes
+// (8 of data, 8 unused).
+bool operand_map(const Operand& o, int64_t pitch, bool packed, int box_rows, CUtensorMap* map) {
+  auto encode = tensor_map_encoder();
+  if (!encode) return false;
+  const bool widen = o.four && !packed;
+  const cuuint64_t row_bytes = static_cast<cuuint64_t>(o.four ? pitch / 2 : pitch);
+  const cuuint64_t dims[2] = {widen ? static_cast<cuuint64_t>(pitch) : row_bytes, static_cast<cuuint64_t>(o.rows)};
+  const cuuint64_t strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(map, widen ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                const_cast<uint8_t*>(o.codes), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int KA, int NT, bool WROWS>
+dbf_status launch_gemm(const Operand& p, const Operand& q, MxArgs a, int64_t pitch, int ks, const DeviceInfo& dev,
+                       cudaStream_t stream) {
+  using C = Cfg<KA, NT, WROWS>;
+  auto kernel = dbf_mx_gemm_kernel<KA, NT, WROWS>;
+  static std::once_flag once[64];  // the attribute once per device
+  static cudaError_t attr_err[64];
+  std::call_once(once[dev.device], [&] {
+    attr_err[dev.device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  });
+  if (attr_err[dev.device] != cudaSuccess) return DBF_ERR_CUDA;
+  CUtensorMap p_map, q_map;
+  if (!operand_map(p, pitch, KA == 2, kRows, &p_map) || !operand_map(q, pitch, KA == 2, NT, &q_map))
+    return DBF_ERR_CUDA;
+  a.p_scales = p.scales;
+  a.q_scales = q.scales;
+  a.p_rows = p.rows;
+  a.q_rows = q.rows;
+  // a widening copy counts the bytes it reads: half of what it fills
+  a.p_tx = KA == 1 && p.four ? kRowBytes / 2 : kRowBytes;
+  a.q_tx = KA == 1 && q.four ? kRowBytes / 2 : kRowBytes;
+  a.idesc = KA == 2 ? idesc_block_scaled(kRows, NT, 1, 1) : idesc_block_scaled(kRows, NT, p.four ? 5 : 0, q.four ? 5 : 0);
+  const int64_t tiles = (p.rows + kRows - 1) / kRows * ((q.rows + NT - 1) / NT);
+  if (tiles * ks > 0x7fffffffLL) return DBF_ERR_UNSUPPORTED_SHAPE;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * ks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(ks);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, p_map, q_map, a) == cudaSuccess ? DBF_OK : DBF_ERR_CUDA;
+}
+
+template <int KA>
+dbf_status launch_mx(const Operand& x, const Operand& w, const MxArgs& base, int64_t pitch, const DeviceInfo& dev,
+                     cudaStream_t stream) {
+  MxArgs a = base;
+  a.stages_k = static_cast<int>((a.k4s + KA - 1) / KA);
+  // tokens x 256 weight rows where those tiles occupy half the SMs; else the
+  // weight's rows by the tokens, the K range split over up to eight CTAs
+  const int64_t wide = (x.rows + kRows - 1) / kRows * ((w.rows + 255) / 256);
+  if (x.rows > 64 && 2 * wide >= dev.num_sms) return launch_gemm<KA, 256, false>(x, w, a, pitch, 1, dev, stream);
+  const int nt = x.rows <= 16 ? 16 : x.rows <= 32 ? 32 : x.rows <= 64 ? 64 : 128;
+  const int64_t tiles = (w.rows + kRows - 1) / kRows * ((x.rows + nt - 1) / nt);
+  int ks = 1;
+  while (ks < 8 && tiles * ks * 2 <= dev.num_sms && ks * 2 <= a.stages_k) ks *= 2;
+  switch (nt) {
+    case 16: return launch_gemm<KA, 16, true>(w, x, a, pitch, ks, dev, stream);
+    case 32: return launch_gemm<KA, 32, true>(w, x, a, pitch, ks, dev, stream);
+    case 64: return launch_gemm<KA, 64, true>(w, x, a, pitch, ks, dev, stream);
+    default: return launch_gemm<KA, 128, true>(w, x, a, pitch, ks, dev, stream);
+  }
+}
+
+constexpr int64_t kMaxReduce = int64_t{1} << 20;
+
+bool forward_shape_ok(int64_t n, int64_t m_in, int64_t batch) {
+  return mx_shape_ok(n, m_in) && mx_shape_ok(batch, m_in) && m_in <= kMaxReduce;
+}
+
+}  // namespace
+}  // namespace dbf
+
+using namespace dbf;
+
+extern "C" {
+
+size_t dbf_mx_forward_workspace_bytes(int64_t n, int64_t m_in, int64_t batch) {
+  return forward_shape_ok(n, m_in, batch) ? kStatusBytes : 0;
+}
+
+dbf_status dbf_mx_forward(const uint8_t* x_codes, const uint8_t* x_scales, dbf_mx_format x_fmt, const uint8_t* w_codes,
+                          const uint8_t* w_scales, dbf_mx_format w_fmt, int64_t n, int64_t m_in, int64_t batch, void* y,
+                          dbf_dtype y_t, void* workspace, size_t ws_bytes, uint32_t flags,
+                          struct CUstream_st* stream) {
+  if (!x_codes || !x_scales || !w_codes || !w_scales || !y) return DBF_ERR_INVALID_ARG;
+  if (!mx_format_ok(x_fmt) || !mx_format_ok(w_fmt) || !float_dtype_ok(y_t)) return DBF_ERR_INVALID_ARG;
+  if (n < 1 || m_in < 1 || batch < 1 || (flags & ~static_cast<uint32_t>(DBF_FWD_WEIGHTS_STATIC)) != 0)
+    return DBF_ERR_INVALID_ARG;
+  if (!forward_shape_ok(n, m_in, batch)) return DBF_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned_to(x_codes, 32) || !aligned_to(w_codes, 32) || !aligned_to(x_scales, 16) || !aligned_to(w_scales, 16) ||
+      !aligned_to(y, 16))
+    return DBF_ERR_MISALIGNED;
+  if (!workspace || !aligned_to(workspace, 16) || ws_bytes < dbf_mx_forward_workspace_bytes(n, m_in, batch))
+    return DBF_ERR_WORKSPACE;
+  DeviceInfo dev;
+  const dbf_status st = current_device(&dev);
+  if (st != DBF_OK) return st;
+  MxArgs a{};
+  a.k4s = mx_pitch(m_in) / 128;
+  a.p_static = (flags & DBF_FWD_WEIGHTS_STATIC) != 0;
+  a.out = y;
+  a.ld_out = n;
+  a.out_t = y_t;
+  a.status = static_cast<int*>(workspace);
+  const Operand x{x_codes, x_scales, batch, x_fmt == DBF_MX_E2M1}, w{w_codes, w_scales, n, w_fmt == DBF_MX_E2M1};
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return x.four && w.four ? launch_mx<2>(x, w, a, mx_pitch(m_in), dev, s) : launch_mx<1>(x, w, a, mx_pitch(m_in), dev, s);
+}
+
+}  // extern "C"

@@ -78,7 +78,8 @@ typedef enum dbf_status {
   DBF_ERR_DEVICE = 7             /* the current device is not an sm_100 (B200-class) GPU */
 } dbf_status;
 
-typedef enum dbf_dtype { DBF_I8 = 0, DBF_F16 = 1, DBF_F32 = 2 } dbf_dtype;
+/* DBF_BF16 is taken by the microscaled and norm calls only. */
+typedef enum dbf_dtype { DBF_I8 = 0, DBF_F16 = 1, DBF_F32 = 2, DBF_BF16 = 3 } dbf_dtype;
 
 /* dbf_forward flags (bitwise OR; 0 is the safe default). */
 enum {
@@ -440,6 +441,124 @@ DBF_API dbf_status dbf_factorize_pass(const float* W, int64_t n, int64_t m, int6
 DBF_API size_t dbf_svid_workspace_bytes(int64_t rows, int64_t cols);
 DBF_API dbf_status dbf_svid(const float* M, int64_t rows, int64_t cols, float* u, float* v, float* sigma,
                             void* workspace, size_t ws_bytes, struct CUstream_st* stream);
+
+/*
+ * Microscaled (MX) matrices (OCP Microscaling Formats, MX v1.0): the weight
+ * format for the layers of a model that do not bear one or two bits, and the
+ * activation format that its product reads.  32 neighbouring columns of a row
+ * form a block; it holds a scale byte s, a factor 2^(s - 127) (255: every value
+ * of the block is NaN), and 32 elements
+ *   DBF_MX_E2M1  4 bits, +-{0, .5, 1, 1.5, 2, 3, 4, 6}
+ *   DBF_MX_E4M3  8 bits, |value| <= 448, 0x7F and 0xFF NaN
+ * A rows x cols matrix is two buffers (the library's own layout):
+ *   codes   dbf_mx_code_bytes(...) bytes, 32-byte aligned: row after row of
+ *           pitch = ceil(cols/128)*128 elements; two E2M1 codes to a byte, the
+ *           even column in the low half.  Codes behind the last column are 0.
+ *   scales  dbf_mx_scale_bytes(...) bytes, 16-byte aligned: 512-byte tiles of
+ *           128 rows x 4 blocks, the tiles of 128 rows one after another along
+ *           the columns.  Row r's block k is byte 16 (r % 32) + 4 (r % 128 / 32)
+ *           + k % 4 of its tile.  Blocks behind the last column are 0; the bytes
+ *           of rows behind the last are never written, and what they hold
+ *           reaches no result.
+ * The tensor cores read codes and scales as they lie there.
+ */
+typedef enum dbf_mx_format { DBF_MX_E2M1 = 0, DBF_MX_E4M3 = 1 } dbf_mx_format;
+
+/* dbf_mx_quantize flags. */
+enum {
+  /* Quantise the transpose: the result is cols x rows, its blocks run down the
+   * columns of src.  For the products that contract over src's rows (the
+   * gradients of a product: dX = dY W needs W's transpose, dW = dY^T X both). */
+  DBF_MX_TRANSPOSE = 1u << 0
+};
+
+/* Bytes of the two buffers of a rows x cols matrix (0 for a size below 1 or
+ * above 1 << 24, for more than 2^40 elements or an unknown format). */
+DBF_API int64_t dbf_mx_code_bytes(int64_t rows, int64_t cols, dbf_mx_format fmt);
+DBF_API int64_t dbf_mx_scale_bytes(int64_t rows, int64_t cols);
+
+/*
+ * Quantise a dense rows x cols matrix (row-major, src_t DBF_F16, DBF_BF16 or
+ * DBF_F32).  Per block, with top = 2 (E2M1) or 8 (E4M3):
+ *     s = clamp(floor(log2(max |x|)) - top, -127, 127), stored as s + 127
+ *     code = round(x 2^-s), to nearest even, saturating at 6 or 448
+ * A block without a finite maximum (an infinity or NaN among its values) gets
+ * scale byte 255 and codes 0; a block of zeros gets scale byte 0.  Exact up to
+ * the one rounding; a partial last block counts only its own columns.
+ *   flags   0 or DBF_MX_TRANSPOSE.
+ *   codes, scales  of a rows x cols (transposed: cols x rows) matrix.
+ * src aligned to its element; codes 32-byte, scales 16-byte aligned; no overlap.
+ * Shape: rows, cols in [1, 1 << 24], at most 2^40 elements either way round.
+ */
+DBF_API dbf_status dbf_mx_quantize(const void* src, dbf_dtype src_t, int64_t rows, int64_t cols, dbf_mx_format fmt,
+                                   uint32_t flags, uint8_t* codes, uint8_t* scales, struct CUstream_st* stream);
+
+/* The values of an MX matrix, rows x cols row-major, dst_t DBF_F16, DBF_BF16 or
+ * DBF_F32 (fp32 is exact; the others round once).  dst aligned to its element. */
+DBF_API dbf_status dbf_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                                     dbf_mx_format fmt, void* dst, dbf_dtype dst_t, struct CUstream_st* stream);
+
+/*
+ * y = X W^T of two MX matrices: X batch x m_in, W n x m_in, each in either
+ * format, on the block-scaled tensor cores (fp32 sums of exact products, the
+ * order of additions fixed by the sizes).  One token to whole prompts.
+ *   y          batch x n row-major, y_t DBF_F16, DBF_BF16 or DBF_F32; 16-byte
+ *              aligned.  A NaN block makes every output of its row NaN.
+ *   workspace  dbf_mx_forward_workspace_bytes(n, m_in, batch) bytes, zero-filled
+ *              before its first use: the status block of dbf_workspace_status.
+ *              Calls that run concurrently may share it.
+ *   flags      0 or DBF_FWD_WEIGHTS_STATIC (w_codes and w_scales are not written
+ *              by work that may still run on `stream`).
+ * Gradients: dX = dY W and dW = dY^T X are this call on transposed operands
+ * (DBF_MX_TRANSPOSE).
+ * Shape: n, batch in [1, 1 << 24], m_in in [1, 1 << 20].
+ */
+DBF_API size_t dbf_mx_forward_workspace_bytes(int64_t n, int64_t m_in, int64_t batch);
+DBF_API dbf_status dbf_mx_forward(const uint8_t* x_codes, const uint8_t* x_scales, dbf_mx_format x_fmt,
+                                  const uint8_t* w_codes, const uint8_t* w_scales, dbf_mx_format w_fmt, int64_t n,
+                                  int64_t m_in, int64_t batch, void* y, dbf_dtype y_t, void* workspace,
+                                  size_t ws_bytes, uint32_t flags, struct CUstream_st* stream);
+
+/*
+ * Root-mean-square norm with the residual's addition, the step in front of a
+ * layer's projections:
+ *     h = round(x + residual);  y = h / sqrt(mean(h^2) + eps) * weight
+ * per row of cols values (fp32 sums; h is rounded to type t before the norm
+ * reads it, so that the residual stream and the norm see the same values).
+ *   x, residual, h   rows x cols of type t (DBF_F16, DBF_BF16, DBF_F32).
+ *              residual and h may both be null: then h = x and is not written.
+ *              h may be x or residual itself; no other overlap.
+ *   weight     cols of type t.
+ *   eps        a normal positive number.
+ * dbf_rmsnorm_forward writes y (rows x cols, type t), the input of
+ * dbf_forward; dbf_rmsnorm_mx_forward quantises y as dbf_mx_quantize does
+ * (without rounding it to t first), the X of dbf_mx_forward.
+ * fp32 rows whose squares overflow fp32 normalise to 0 (or NaN).
+ * Pointers aligned to their element (codes 32, scales 16 bytes).
+ * Shape: rows in [1, 1 << 24], cols in [1, 1 << 20], at most 2^40 elements.
+ */
+DBF_API dbf_status dbf_rmsnorm_forward(const void* x, const void* residual, const void* weight, dbf_dtype t,
+                                       int64_t rows, int64_t cols, float eps, void* h, void* y,
+                                       struct CUstream_st* stream);
+DBF_API dbf_status dbf_rmsnorm_mx_forward(const void* x, const void* residual, const void* weight, dbf_dtype t,
+                                          int64_t rows, int64_t cols, float eps, dbf_mx_format fmt, void* h,
+                                          uint8_t* codes, uint8_t* scales, struct CUstream_st* stream);
+
+/*
+ * Gradients of the norm (a quantised output counts as its unrounded value).
+ * With rstd = 1 / sqrt(mean(h^2) + eps) and g = dy weight:
+ *     dx = rstd g - h rstd^3 mean(g h) + dh      (x's and the residual's gradient)
+ *     dweight = sum over rows of dy h rstd
+ *   dy, h, dh, dx   rows x cols of type t; dh, the gradient that reaches h by the
+ *              residual stream, may be null.  dx may be dh or dy; no other overlap.
+ *   dweight    cols fp32 (the sum's order is fixed by the sizes).
+ *   workspace  dbf_rmsnorm_backward_workspace_bytes(rows, cols) bytes; need not be
+ *              zeroed.  Calls that run concurrently need distinct workspaces.
+ */
+DBF_API size_t dbf_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
+DBF_API dbf_status dbf_rmsnorm_backward(const void* dy, const void* h, const void* weight, const void* dh, dbf_dtype t,
+                                        int64_t rows, int64_t cols, float eps, void* dx, float* dweight,
+                                        void* workspace, size_t ws_bytes, struct CUstream_st* stream);
 
 /* Static, NUL-terminated description of a status code. */
 DBF_API const char* dbf_status_string(dbf_status status);

@@ -1,0 +1,262 @@
+"""GPU parity of the microscaled quantisation and product through the public calls, against the fp64 reference
+(oracle/mx.py).
+
+Quantisation is exact: codes and scale bytes must be equal.  The product's tolerance: the K exact products are added
+in fp32, in any order and with truncation (each of the at most K additions is off by at most 2^-23 of the running sum
+of magnitudes), so |err| <= K 2^-23 sum|x w|, plus half a step of the result's type.  Integer data (every partial sum
+a whole number below 2^24) must come out exact."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import mx
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"fp16": torch.float16, "bf16": torch.bfloat16, "fp32": torch.float32}
+STEP = {"fp16": 2.0 ** -11, "bf16": 2.0 ** -8, "fp32": 2.0 ** -24}
+
+
+@pytest.fixture(scope="module")
+def dbf():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from binary_factorized_weight_b200 import build
+
+    build.build()
+    import binary_factorized_weight_b200 as mod
+
+    mod.load_library()
+    return mod
+
+
+def host(t):
+    return t.detach().double().cpu().numpy() if t.is_floating_point() else t.cpu().numpy()
+
+
+def held(v, fmt):
+    """A matrix in the library's buffers, made by the reference: (codes, scales) on the GPU."""
+    code, byte = mx.quantize(v, fmt)
+    return (torch.from_numpy(mx.pack_codes(code, fmt)).cuda(),
+            torch.from_numpy(mx.pack_scales(byte, *v.shape)).cuda())
+
+
+def assert_held(codes, scales, v, fmt):
+    rows, cols = v.shape
+    code, byte = mx.quantize(v, fmt)
+    np.testing.assert_array_equal(mx.unpack_scales(host(scales), rows, cols), byte)
+    np.testing.assert_array_equal(mx.unpack_codes(host(codes), rows, cols, fmt), code)
+
+
+def source(rows, cols, kind, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    v = torch.randn(rows, cols, generator=g) * torch.exp2(torch.randint(-12, 12, (rows, 1), generator=g).float())
+    return v.to(TYPES[kind]).cuda()
+
+
+@pytest.mark.parametrize("fmt", [mx.E2M1, mx.E4M3])
+@pytest.mark.parametrize("kind", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 4096), (3, 31), (130, 33), (257, 520), (64, 1000), (127, 129)])
+def test_quantize_is_exact(dbf, rows, cols, kind, fmt):
+    v = source(rows, cols, kind)
+    codes, scales = dbf.dbf_mx_quantize(v, fmt)
+    assert_held(codes, scales, host(v), fmt)
+    codes, scales = dbf.dbf_mx_quantize(v, fmt, transpose=True)
+    assert_held(codes, scales, np.ascontiguousarray(host(v).T), fmt)
+
+
+@pytest.mark.parametrize("fmt", [mx.E2M1, mx.E4M3])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_quantize_borders_and_special_values(dbf, fmt, transpose):
+    rng = np.random.default_rng(3)
+    grid = mx.values(fmt)
+    mid = (grid[1:] + grid[:-1]) / 2
+    near = np.concatenate([grid, mid, np.nextafter(mid.astype(np.float32), np.float32(0)).astype(np.float64),
+                           np.nextafter(mid.astype(np.float32), np.float32(9e9)).astype(np.float64)])
+    rows = [rng.permutation(np.resize(near, 320)) * rng.choice([-1, 1], 320) * 2.0 ** e
+            for e in (-126, -100, -20, 0, 3, 100, 110)]
+    rows += [np.resize(2.0 ** -149 * np.arange(9), 320), np.zeros(320), np.full(320, -0.0), np.full(320, 3.4028234e38)]
+    v = np.array(rows).astype(np.float32)
+    v[2, 40] = np.nan
+    v[3, 70] = np.inf
+    v[4, 319] = -np.inf
+    t = torch.from_numpy(v).cuda()
+    codes, scales = dbf.dbf_mx_quantize(t.t().contiguous() if transpose else t, fmt, transpose=transpose)
+    assert_held(codes, scales, v.astype(np.float64), fmt)
+    back = host(dbf.dbf_mx_dequantize(codes, scales, *v.shape, fmt))
+    code, byte = mx.quantize(v, fmt)
+    np.testing.assert_array_equal(back, mx.dequantize(code, byte, 320, fmt))
+
+
+@pytest.mark.parametrize("fmt", [mx.E2M1, mx.E4M3])
+@pytest.mark.parametrize("kind", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (5, 100), (130, 256), (129, 1001)])
+def test_dequantize(dbf, rows, cols, kind, fmt):
+    v = host(source(rows, cols, "fp32", seed=1))
+    got = dbf.dbf_mx_dequantize(*held(v, fmt), rows, cols, fmt, dtype=TYPES[kind])
+    want = torch.from_numpy(mx.dequantize(*mx.quantize(v, fmt), cols, fmt)).float().to(TYPES[kind])
+    assert got.dtype == TYPES[kind] and torch.equal(got.cpu(), want)
+
+
+def test_every_code(dbf):
+    codes = np.arange(256).reshape(2, 128)
+    byte = np.array([[0, 1, 127, 253], [255, 130, 120, 64]])
+    got = host(dbf.dbf_mx_dequantize(torch.from_numpy(codes.astype(np.uint8)).cuda().view(-1),
+                                     torch.from_numpy(mx.pack_scales(byte, 2, 128)).cuda(), 2, 128, mx.E4M3))
+    with np.errstate(over="ignore"):
+        want = mx.dequantize(codes, byte, 128, mx.E4M3).astype(np.float32).astype(np.float64)
+    np.testing.assert_array_equal(got, want)
+
+
+def product(dbf, X, W, xf, wf, kind, **more):
+    return dbf.dbf_mx_forward(*held(X, xf), *held(W, wf), W.shape[0], W.shape[1], X.shape[0], x_fmt=xf, w_fmt=wf,
+                              y_dtype=TYPES[kind], **more)
+
+
+def assert_product(y, X, W, xf, wf, kind):
+    x = mx.dequantize(*mx.quantize(X, xf), X.shape[1], xf)
+    w = mx.dequantize(*mx.quantize(W, wf), W.shape[1], wf)
+    want = x @ w.T
+    tol = X.shape[1] * 2.0 ** -23 * (np.abs(x) @ np.abs(w).T) + STEP[kind] * np.abs(want) + 2.0 ** -25
+    assert (np.abs(host(y) - want) <= tol).all(), np.max(np.abs(host(y) - want) / tol)
+
+
+FORMATS = [(mx.E2M1, mx.E2M1), (mx.E4M3, mx.E2M1), (mx.E4M3, mx.E4M3), (mx.E2M1, mx.E4M3)]
+SHAPES = [(1, 128, 128), (1, 1, 1), (3, 100, 33), (16, 256, 512), (17, 130, 640), (33, 1000, 300), (64, 129, 1111),
+          (65, 257, 700), (100, 64, 4096), (200, 300, 520), (1, 4096, 4096), (130, 96, 129)]
+
+
+@pytest.mark.parametrize("xf,wf", FORMATS)
+@pytest.mark.parametrize("batch,n,m_in", SHAPES)
+def test_integer_product_is_exact(dbf, batch, n, m_in, xf, wf):
+    rng = np.random.default_rng(batch + n + m_in)
+    X = rng.choice([0.0, 1, 2, 3, 4, 6, -1, -2, -6], (batch, m_in))
+    W = rng.choice([0.0, 1, -1, 2, -3, 6], (n, m_in)) * 2.0 ** rng.integers(-1, 3, (n, 1))
+    X[:, 0::32] = 6  # every block's largest value: nothing is lost
+    W[:, 0::32] = 6
+    assert (mx.dequantize(*mx.quantize(X, xf), m_in, xf) == X).all()
+    y = product(dbf, X, W, xf, wf, "fp32")
+    w = mx.dequantize(*mx.quantize(W, wf), m_in, wf)
+    np.testing.assert_array_equal(host(y), X @ w.T)
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16", "fp32"])
+@pytest.mark.parametrize("xf,wf", FORMATS)
+@pytest.mark.parametrize("batch,n,m_in", [(1, 300, 1000), (16, 1024, 4096), (77, 501, 1111), (300, 640, 1500), (2, 77, 5000)])
+def test_product(dbf, batch, n, m_in, xf, wf, kind):
+    rng = np.random.default_rng(n)
+    X = rng.standard_normal((batch, m_in)) * np.where(rng.random(m_in) < 0.01, 30, 1)
+    W = rng.standard_normal((n, m_in)) * 0.05
+    assert_product(product(dbf, X, W, xf, wf, kind), X, W, xf, wf, kind)
+
+
+@pytest.mark.parametrize("xf,wf", FORMATS)
+@pytest.mark.parametrize("batch,n,m_in", [(2048, 2500, 384), (1000, 4736, 130), (260, 14336, 256)])
+def test_many_tiles(dbf, batch, n, m_in, xf, wf):
+    rng = np.random.default_rng(9)
+    X, W = rng.standard_normal((batch, m_in)), rng.standard_normal((n, m_in)) * 0.05
+    assert_product(product(dbf, X, W, xf, wf, "fp16"), X, W, xf, wf, "fp16")
+
+
+@pytest.mark.parametrize("batch", [1, 40, 300])
+@pytest.mark.parametrize("xf,wf", FORMATS)
+def test_nan_blocks_stay_in_their_rows(dbf, batch, xf, wf):
+    rng = np.random.default_rng(2)
+    X, W = rng.standard_normal((batch, 300)), rng.standard_normal((600, 300))
+    X[batch // 2, 290] = np.inf
+    W[7, 3] = np.nan
+    y = host(product(dbf, X, W, xf, wf, "fp32"))
+    bad = np.zeros((batch, 600), bool)
+    bad[batch // 2] = True
+    bad[:, 7] = True
+    np.testing.assert_array_equal(np.isnan(y), bad)
+    assert np.isfinite(y[~bad]).all()
+
+
+@pytest.mark.parametrize("xf,wf", FORMATS)
+def test_scale_range(dbf, xf, wf):
+    """Blocks whose scales lie far apart: the sum is exact where one block carries it all."""
+    X, W = np.zeros((2, 128)), np.zeros((3, 128))
+    X[:, :] = 2.0 ** -60
+    W[:, :] = 2.0 ** -50
+    X[1, 32:64] = 2.0 ** 60
+    W[2, 32:64] = 2.0 ** 50
+    y = host(product(dbf, X, W, xf, wf, "fp32"))
+    x, w = X.astype(np.float64), W.astype(np.float64)
+    np.testing.assert_allclose(y, x @ w.T, rtol=2.0 ** -20)
+
+
+def test_one_long_token(dbf):
+    """m_in at a million.  Normal data: the running sum stays below about 4 sqrt(K) = 2^12, an addition for each 32 of K
+    loses at most 2^-23 of it: 2^15 2^-23 2^12 = 2^4; the bound allows four times that, 2^-14 |x| |w| = 2^6."""
+    rng = np.random.default_rng(4)
+    X, W = rng.standard_normal((2, 1 << 20)), rng.standard_normal((5, 1 << 20))
+    for xf, wf in FORMATS[:2]:
+        x, w = mx.dequantize(*mx.quantize(X, xf), 1 << 20, xf), mx.dequantize(*mx.quantize(W, wf), 1 << 20, wf)
+        y = host(product(dbf, X, W, xf, wf, "fp32"))
+        assert (np.abs(y - x @ w.T) <= 2.0 ** -14 * np.sqrt((x * x).sum(1)[:, None] * (w * w).sum(1)[None, :])).all()
+
+
+@pytest.mark.parametrize("batch", [1, 20, 100, 300])
+def test_nothing_outside_y_is_written(dbf, batch):
+    rng = np.random.default_rng(8)
+    n, m_in = 333, 200
+    X, W = rng.standard_normal((batch, m_in)), rng.standard_normal((n, m_in))
+    whole = torch.full((batch * n + 64,), 7.0, dtype=torch.float32, device="cuda")
+    product(dbf, X, W, mx.E4M3, mx.E2M1, "fp32", y=whole[: batch * n].view(batch, n))
+    assert (whole[batch * n:] == 7).all()
+
+
+def test_streams_graph_and_shared_workspace(dbf):
+    """Calls on two streams and in replayed graphs share one workspace; results equal the plain call's."""
+    rng = np.random.default_rng(1)
+    n, m_in = 700, 900
+    W = held(rng.standard_normal((n, m_in)), mx.E2M1)
+    ws = dbf.dbf_mx_new_workspace(n, m_in, 8)
+    xs = [held(rng.standard_normal((8, m_in)), mx.E4M3) for _ in range(2)]
+    call = lambda x, **k: dbf.dbf_mx_forward(*x, *W, n, m_in, 8, workspace=ws, flags=dbf.DBF_FWD_WEIGHTS_STATIC, **k)  # noqa: E731
+    want = [call(x).clone() for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [call(x, stream=s) for x, s in zip(xs, streams)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graphs, outs = [], []
+    for x in xs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(call(x))
+        graphs.append(g)
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert dbf.dbf_workspace_status(ws) == 0
+
+
+def test_results_repeat_bit_for_bit(dbf):
+    rng = np.random.default_rng(12)
+    for batch in (1, 16, 128, 600):
+        X, W = held(rng.standard_normal((batch, 2000)), mx.E4M3), held(rng.standard_normal((1500, 2000)), mx.E2M1)
+        first = dbf.dbf_mx_forward(*X, *W, 1500, 2000, batch, y_dtype=torch.float32)
+        for _ in range(5):
+            assert torch.equal(first, dbf.dbf_mx_forward(*X, *W, 1500, 2000, batch, y_dtype=torch.float32))
+
+
+def test_refusals_of_the_binding(dbf):
+    x = torch.zeros(4, 64, device="cuda")
+    codes, scales = dbf.dbf_mx_quantize(x, mx.E2M1)
+    with pytest.raises(ValueError):
+        dbf.dbf_mx_quantize(x.t(), mx.E2M1)  # not contiguous
+    with pytest.raises(ValueError):
+        dbf.dbf_mx_quantize(x, 5)
+    with pytest.raises(ValueError):
+        dbf.dbf_mx_dequantize(codes, scales, 5, 64, mx.E2M1)  # buffers too small
+    with pytest.raises(ValueError):
+        dbf.dbf_mx_forward(codes, scales, codes, scales, 4, 64, 4, x_fmt=mx.E4M3, w_fmt=mx.E2M1)
+    with pytest.raises(TypeError):
+        dbf.dbf_mx_forward(codes, scales, codes, scales, 4, 64, 4, x_fmt=0, w_fmt=0, y_dtype=torch.float64)
+    with pytest.raises(dbf.DBFError):
+        dbf.dbf_mx_forward(codes, scales, codes, scales, 4, 64, 4, x_fmt=0, w_fmt=0, flags=1 << 5)
