@@ -316,6 +316,310 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// ---------------------------------------------------------------- many tiles: CTA pairs
+// Tiles of 256 tokens x NT weight rows, one per pair of CTAs (cta_group::2): each
+// CTA holds its 128 tokens and half of the tile's weight rows, so a stage costs
+// it 16 KB + NT/2 rows where a CTA alone would fetch NT; the MMA reads both.
+// The pairs are persistent (one CTA per SM) and walk the tiles, tokens fastest;
+// the ring runs on across tiles.  Accumulators: tensor memory holds two of NT
+// columns that overlap in their last / first columns where both do not fit
+// beside the scales, so the MMAs of a tile wait only until the epilogue has
+// read the shared columns of the tile before.
+// The epilogue writes through shared memory with TMA stores (rows of y on 16
+// bytes), else row by row.
+template <int KA, int NT>
+struct PairCfg {
+  static constexpr int kQRows = NT / 2;
+  static constexpr int kQTiles = NT % 128 == 0 ? NT / 128 : (NT + 96 + 127) / 128;  // scale tiles a tile's rows touch
+  static constexpr int kPBytes = kRows * kRowBytes;
+  static constexpr int kQBytes = kQRows * kRowBytes;
+  static constexpr int kScaleBytes = KA * (1 + kQTiles) * kTileBytes;
+  static constexpr int kStageBytes = kPBytes + kQBytes + kScaleBytes;
+  static constexpr int kWarpBuf = 32 * 128;  // 32 rows x 128 bytes
+  static constexpr int kBufs = 3;            // per epilogue warp
+  static constexpr int kEpiBytes = 4 * kBufs * kWarpBuf;
+  static constexpr int kRoom = 227 * 1024 - 1024 - 512 - kEpiBytes;
+  static constexpr int kStages = kRoom / kStageBytes < 6 ? kRoom / kStageBytes : 6;
+  static constexpr int kEpiOffset = kStages * (kPBytes + kQBytes);
+  static constexpr int kScaleOffset = kEpiOffset + kEpiBytes;
+  static constexpr int kBarOffset = kScaleOffset + kStages * kScaleBytes;
+  static constexpr int kSmemBytes = kBarOffset + 512 + 1024;
+  static constexpr int kScaleCols = 4 * KA * (1 + kQTiles);
+  static constexpr int kScaleBase = 512 - kScaleCols;
+  // the second accumulator starts where it still ends before the scales
+  static constexpr int kAcc1 = 2 * NT <= kScaleBase ? NT : (kScaleBase - NT) / 32 * 32;
+  static constexpr int kShared = NT - kAcc1;  // columns both accumulators use
+  static_assert(kShared % 32 == 0 && kShared <= 64, "");
+};
+
+struct PairArgs {
+  int64_t p_rows, q_rows;
+  int64_t k4s;
+  int stages_k;
+  int tx;  // bytes of a stage, both CTAs
+  uint32_t idesc;
+  int w_static;
+  void* out;
+  int64_t ld_out;
+  int out_t;
+  int tma_out;
+  int* status;
+};
+
+template <int KA, int NT>
+__global__ void __launch_bounds__(kThreads, 1)
+    dbf_mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
+                            const __grid_constant__ CUtensorMap ps_map, const __grid_constant__ CUtensorMap qs_map,
+                            const __grid_constant__ CUtensorMap y_map, const PairArgs a) {
+  using C = PairCfg<KA, NT>;
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* p_st = smem;
+  uint8_t* q_st = smem + S * C::kPBytes;
+  uint8_t* epi_st = smem + C::kEpiOffset;
+  uint8_t* s_st = smem + C::kScaleOffset;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);  // the even CTA's count both CTAs' bytes
+  uint64_t* empty = full + S;
+  uint64_t* acc_full = empty + S;   // one per accumulator
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* acc_shared = acc_empty + 2;  // the columns that the accumulators share have been read
+  uint64_t* mma_done = acc_shared + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const int64_t p_tiles = (a.p_rows + 255) / 256;
+  const int64_t tiles = p_tiles * ((a.q_rows + NT - 1) / NT);
+  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 8);  // the epilogue warps of both CTAs
+      mbar_init(&acc_shared[i], 8);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tmap(&p_map);
+    prefetch_tmap(&q_map);
+    prefetch_tmap(&ps_map);
+    prefetch_tmap(&qs_map);
+    if (a.tma_out) prefetch_tmap(&y_map);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  // no copy, MMA or arrival reaches the other CTA before its barriers stand
+  cluster_arrive_release();
+  cluster_wait_acquire();
+  tc_fence_after();
+  pdl_launch_dependents();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------ TMA producer (each CTA its own halves)
+    if (lane == 0) {
+      bool ok = true;
+      uint32_t it = 0;
+      pdl_wait();
+      for (int64_t t = pair; t < tiles && ok; t += pairs) {
+        const int p0 = static_cast<int>((t % p_tiles) * 256) + rank * kRows;
+        const int64_t q0 = (t / p_tiles) * NT;
+        for (int kt = 0; kt < a.stages_k; ++kt, ++it) {
+          const int s = static_cast<int>(it % S);
+          if (it >= S && !mbar_wait_pair(&empty[s], (it / S - 1) & 1, abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], a.tx);
+          const uint32_t bar = map_to_rank(&full[s], 0);
+          uint8_t* sc = s_st + s * C::kScaleBytes;
+          tma_load_2d_pair(p_st + s * C::kPBytes, &p_map, kt * 128, p0, bar);
+          tma_load_2d_pair(q_st + s * C::kQBytes, &q_map, kt * 128, static_cast<int>(q0) + rank * C::kQRows, bar);
+          tma_load_2d_pair(sc, &ps_map, kt * 128 * KA, p0 >> 7, bar);
+          tma_load_2d_pair(sc + KA * kTileBytes, &qs_map, kt * 128 * KA, static_cast<int>(q0 >> 7), bar);
+        }
+      }
+      // after a wait that gave up: no copy may still be on its way when the CTAs end
+      if (*abort_flag && rank == 0) {
+        int never = 0;
+        for (uint32_t i = it < S ? 0 : it - S; i < it; ++i)
+          (void)mbar_wait_pair(&full[i % S], (i / S) & 1, &never, a.status);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------ scale copies and MMAs (the even CTA's, for both)
+    if (lane == 0 && rank == 0) {
+      bool ok = true;
+      uint32_t it = 0, n = 0;
+      for (int64_t t = pair; t < tiles && ok; t += pairs, ++n) {
+        const uint32_t b = n & 1, use = n >> 1;
+        // this accumulator's last tile has been read, and the tile before has
+        // left the shared columns
+        if (n >= 2) ok = mbar_wait_pair(&acc_empty[b], (use - 1) & 1, abort_flag, a.status);
+        if (C::kShared > 0 && n >= 1 && ok)
+          ok = mbar_wait_pair(&acc_shared[b ^ 1], ((n - 1) >> 1) & 1, abort_flag, a.status);
+        if (!ok) break;
+        const uint32_t d = tmem + b * C::kAcc1;
+        const uint32_t sfa = tmem + C::kScaleBase, sfb = sfa + 4 * KA;
+        // where the tile's first weight row lies in its scale tile
+        const uint32_t q_col = static_cast<uint32_t>(((t / p_tiles) * NT & 127) >> 5);
+        for (int kt = 0; kt < a.stages_k; ++kt, ++it) {
+          const int s = static_cast<int>(it % S);
+          if (!mbar_wait_pair(&full[s], (it / S) & 1, abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sc = smem_u32(s_st + s * C::kScaleBytes);
+#pragma unroll
+          for (int k = 0; k < KA; ++k) {
+            tc_copy_scales_pair(sfa + 4 * k, smem_desc_rows16(sc + k * kTileBytes));
+#pragma unroll
+            for (int j = 0; j < C::kQTiles; ++j)
+              tc_copy_scales_pair(sfb + 4 * (k * C::kQTiles + j), smem_desc_rows16(sc + (KA * (1 + j) + k) * kTileBytes));
+          }
+          const uint32_t pa = smem_u32(p_st + s * C::kPBytes), qa = smem_u32(q_st + s * C::kQBytes);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint32_t acc = kt != 0 || kk != 0 ? 1u : 0u;
+            const uint64_t pd = smem_desc_sw128_kmajor(pa + kk * 32), qd = smem_desc_sw128_kmajor(qa + kk * 32);
+            if constexpr (KA == 2) {
+              const uint32_t id = 2u * (kk & 1);
+              tc_mma_mxf4_pair(d, pd, qd, a.idesc | (id << 4) | (id << 29), sfa + 4 * (kk >> 1),
+                               sfb + q_col + 4 * C::kQTiles * (kk >> 1), acc);
+            } else {
+              tc_mma_mxf8f6f4_pair(d, pd, qd,
+                                   a.idesc | (static_cast<uint32_t>(kk) << 4) | (static_cast<uint32_t>(kk) << 29), sfa,
+                                   sfb + q_col, acc);
+            }
+          }
+          tc_commit_pair(&empty[s]);
+        }
+        if (ok) tc_commit_pair(&acc_full[b]);
+      }
+      tc_commit_pair(mma_done);
+    }
+  } else {
+    // ------------------------------------------------ epilogue
+    const int q = warp & 3;  // the TMEM lanes this warp may read
+    uint8_t* buf = epi_st + q * (C::kBufs * C::kWarpBuf);
+    const int cols = a.out_t == DBF_F32 ? 32 : 64;  // of 128 bytes
+    uint32_t n = 0, stores = 0;
+    for (int64_t t = pair; t < tiles; t += pairs, ++n) {
+      const uint32_t b = n & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait_pair(&acc_full[b], (n >> 1) & 1, abort_flag, a.status))) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * C::kAcc1;
+      const int64_t row0 = (t % p_tiles) * 256 + rank * kRows + q * 32, q0 = (t / p_tiles) * NT;
+      const int rows = static_cast<int>(max(int64_t{0}, min(int64_t{32}, a.p_rows - row0)));
+      // the columns shared with the other accumulator first: the last ones of
+      // accumulator 0, the first of accumulator 1
+      for (int i = 0; i < NT / cols; ++i) {
+        const int c0 = b == 0 && C::kShared > 0 ? NT - (i + 1) * cols : i * cols;
+        uint8_t* dst = buf + (stores % C::kBufs) * C::kWarpBuf;
+        // the store that last used this buffer has read it
+        if (lane == 0) bulk_wait_read<C::kBufs - 1>();
+        __syncwarp();
+        uint32_t v[32];
+        // 16-byte chunk c of row r lies at chunk c ^ (r & 7): the TMA map's swizzle
+        uint8_t* line = dst + lane * 128;
+        if (a.out_t == DBF_F32) {
+          tmem_ld_32x32b_x32(acc + c0, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(line + ((j ^ (lane & 7)) << 4)) =
+                make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            tmem_ld_32x32b_x32(acc + c0 + 32 * h, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float lo = __uint_as_float(v[8 * j + 2 * e]), hi = __uint_as_float(v[8 * j + 2 * e + 1]);
+                if (a.out_t == DBF_F16) {
+                  const __half2 p2 = __floats2half2_rn(lo, hi);
+                  w[e] = *reinterpret_cast<const uint32_t*>(&p2);
+                } else {
+                  const __nv_bfloat162 p2 = __floats2bfloat162_rn(lo, hi);
+                  w[e] = *reinterpret_cast<const uint32_t*>(&p2);
+                }
+              }
+              *reinterpret_cast<uint4*>(line + (((4 * h + j) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        if (C::kShared > 0 && (i + 1) * cols == (C::kShared + cols - 1) / cols * cols) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote_release(map_to_rank(&acc_shared[b], 0));
+        }
+        if (i + 1 == NT / cols) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote_release(map_to_rank(&acc_empty[b], 0));
+        }
+        if (a.tma_out) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (rows > 0 && q0 + c0 < a.q_rows) tma_store_2d(&y_map, dst, static_cast<int>(q0) + c0, static_cast<int>(row0));
+            bulk_commit_group();
+          }
+          ++stores;
+        } else {
+          __syncwarp();
+          const int64_t left = a.q_rows - q0 - c0;
+          const int lim = static_cast<int>(min(static_cast<int64_t>(cols), left));
+          for (int r = 0; r < rows; ++r) {
+            const uint8_t* src = dst + r * 128;
+            for (int c = lane; c < lim; c += 32) {
+              if (a.out_t == DBF_F32) {
+                static_cast<uint32_t*>(a.out)[(row0 + r) * a.ld_out + q0 + c0 + c] =
+                    *reinterpret_cast<const uint32_t*>(src + (((c >> 2) ^ (r & 7)) << 4) + 4 * (c & 3));
+              } else {
+                static_cast<uint16_t*>(a.out)[(row0 + r) * a.ld_out + q0 + c0 + c] =
+                    *reinterpret_cast<const uint16_t*>(src + (((c >> 3) ^ (r & 7)) << 4) + 2 * (c & 7));
+              }
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all<0>();
+    __syncwarp();
+  }
+
+  // ------------------------------------------------ teardown
+  __syncwarp();
+  tc_fence_before();
+  if (warp == 1) (void)mbar_wait_pair(mma_done, 0, abort_flag, a.status);
+  // neither CTA ends while the other may still read its memory or signal it
+  cluster_arrive_release();
+  cluster_wait_acquire();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
 // ---------------------------------------------------------------- host
 struct Operand {
   const uint8_t* codes;
@@ -383,15 +687,91 @@ dbf_status launch_gemm(const Operand& p, const Operand& q, MxArgs a, int64_t pit
   return cudaLaunchKernelEx(&cfg, kernel, p_map, q_map, a) == cudaSuccess ? DBF_OK : DBF_ERR_CUDA;
 }
 
+// The map of one operand's scale tiles, as 32-bit words.
+bool scale_map(const Operand& o, int64_t k4s, int ka, int box_tiles, CUtensorMap* map) {
+  auto encode = tensor_map_encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k4s * 128), static_cast<cuuint64_t>((o.rows + 127) / 128)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(k4s * kTileBytes)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 * ka), static_cast<cuuint32_t>(box_tiles)};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(o.scales), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The map of y for stores of 32 rows x 128 bytes.
+bool out_map(void* y, int out_t, int64_t rows, int64_t cols, CUtensorMap* map) {
+  auto encode = tensor_map_encoder();
+  if (!encode) return false;
+  const size_t e = dtype_size(out_t);
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * e};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / e), 32};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapDataType t = out_t == DBF_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                : out_t == DBF_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return encode(map, t, 2, y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int KA, int NT>
+dbf_status launch_pair(const Operand& x, const Operand& w, const MxArgs& m, int64_t pitch, const DeviceInfo& dev,
+                       cudaStream_t stream) {
+  using C = PairCfg<KA, NT>;
+  auto kernel = dbf_mx_gemm_pair_kernel<KA, NT>;
+  static std::once_flag once[64];  // the attribute once per device
+  static cudaError_t attr_err[64];
+  std::call_once(once[dev.device], [&] {
+    attr_err[dev.device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  });
+  if (attr_err[dev.device] != cudaSuccess) return DBF_ERR_CUDA;
+  PairArgs a{};
+  a.p_rows = x.rows;
+  a.q_rows = w.rows;
+  a.k4s = m.k4s;
+  a.stages_k = m.stages_k;
+  const int p_tx = KA == 1 && x.four ? kRowBytes / 2 : kRowBytes, q_tx = KA == 1 && w.four ? kRowBytes / 2 : kRowBytes;
+  a.tx = 2 * (kRows * p_tx + C::kQRows * q_tx + C::kScaleBytes);
+  a.idesc = KA == 2 ? idesc_block_scaled(256, NT, 1, 1) : idesc_block_scaled(256, NT, x.four ? 5 : 0, w.four ? 5 : 0);
+  a.out = m.out;
+  a.ld_out = m.ld_out;
+  a.out_t = m.out_t;
+  a.status = m.status;
+  a.tma_out = m.ld_out * static_cast<int64_t>(dtype_size(m.out_t)) % 16 == 0;
+  CUtensorMap p_map, q_map, ps_map, qs_map, y_map{};
+  if (!operand_map(x, pitch, KA == 2, kRows, &p_map) || !operand_map(w, pitch, KA == 2, C::kQRows, &q_map) ||
+      !scale_map(x, m.k4s, KA, 1, &ps_map) || !scale_map(w, m.k4s, KA, C::kQTiles, &qs_map) ||
+      (a.tma_out && !out_map(m.out, m.out_t, x.rows, w.rows, &y_map)))
+    return DBF_ERR_CUDA;
+  const int64_t tiles = (x.rows + 255) / 256 * ((w.rows + NT - 1) / NT);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, dev.num_sms / 2)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, p_map, q_map, ps_map, qs_map, y_map, a) == cudaSuccess ? DBF_OK : DBF_ERR_CUDA;
+}
+
 template <int KA>
 dbf_status launch_mx(const Operand& x, const Operand& w, const MxArgs& base, int64_t pitch, const DeviceInfo& dev,
                      cudaStream_t stream) {
   MxArgs a = base;
   a.stages_k = static_cast<int>((a.k4s + KA - 1) / KA);
-  // tokens x 256 weight rows where those tiles occupy half the SMs; else the
+  // 256 tokens x 256 weight rows where those tiles occupy half the pairs; else the
   // weight's rows by the tokens, the K range split over up to eight CTAs
-  const int64_t wide = (x.rows + kRows - 1) / kRows * ((w.rows + 255) / 256);
-  if (x.rows > 64 && 2 * wide >= dev.num_sms) return launch_gemm<KA, 256, false>(x, w, a, pitch, 1, dev, stream);
+  const int64_t wide = (x.rows + 255) / 256 * ((w.rows + 255) / 256);
+  if (x.rows > 64 && 4 * wide >= dev.num_sms) return launch_pair<KA, 256>(x, w, a, pitch, dev, stream);
   const int nt = x.rows <= 16 ? 16 : x.rows <= 32 ? 32 : x.rows <= 64 ? 64 : 128;
   const int64_t tiles = (w.rows + kRows - 1) / kRows * ((x.rows + nt - 1) / nt);
   int ks = 1;

@@ -150,12 +150,28 @@ def test_product(dbf, batch, n, m_in, xf, wf, kind):
     assert_product(product(dbf, X, W, xf, wf, kind), X, W, xf, wf, kind)
 
 
+@pytest.mark.parametrize("kind", ["fp16", "fp32"])
 @pytest.mark.parametrize("xf,wf", FORMATS)
-@pytest.mark.parametrize("batch,n,m_in", [(2048, 2500, 384), (1000, 4736, 130), (260, 14336, 256)])
-def test_many_tiles(dbf, batch, n, m_in, xf, wf):
+@pytest.mark.parametrize("batch,n,m_in", [(2048, 2504, 384), (1000, 4737, 130), (260, 14336, 256), (65, 19001, 100),
+                                          (1024, 2400, 2100)])
+def test_many_tiles(dbf, batch, n, m_in, xf, wf, kind):
     rng = np.random.default_rng(9)
     X, W = rng.standard_normal((batch, m_in)), rng.standard_normal((n, m_in)) * 0.05
-    assert_product(product(dbf, X, W, xf, wf, "fp16"), X, W, xf, wf, "fp16")
+    whole = torch.full((batch * n + 64,), 7.0, dtype=TYPES[kind], device="cuda")
+    y = product(dbf, X, W, xf, wf, kind, y=whole[: batch * n].view(batch, n))
+    assert_product(y, X, W, xf, wf, kind)
+    assert (whole[batch * n:] == 7).all()
+
+
+@pytest.mark.parametrize("xf,wf", FORMATS)
+def test_many_tiles_integer_exact(dbf, xf, wf):
+    """Several tiles per CTA pair, every row and column with a scale of its own."""
+    rng = np.random.default_rng(10)
+    batch, n, m_in = 1100, 5000, 700
+    X = rng.choice([0.0, 1, 2, 3, -1, -2, -6], (batch, m_in)) * 2.0 ** rng.integers(-2, 3, (batch, 1))
+    W = rng.choice([0.0, 1, -1, 2, -3], (n, m_in)) * 2.0 ** rng.integers(-2, 3, (n, 1))
+    x, w = mx.dequantize(*mx.quantize(X, xf), m_in, xf), mx.dequantize(*mx.quantize(W, wf), m_in, wf)
+    np.testing.assert_array_equal(host(product(dbf, X, W, xf, wf, "fp32")), x @ w.T)
 
 
 @pytest.mark.parametrize("batch", [1, 40, 300])
