@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer
-    if (lane == 0) {
+    if (elect_one()) {
       // scale tiles of Q's rows that exist (the last tile of rows may stand alone)
       const int q_tiles = static_cast<int>(min(static_cast<int64_t>(C::kQTiles), (a.q_rows - q0 + 127) >> 7));
       auto load_p = [&](int kt, int s) {
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------ scale copies and MMAs
-    if (lane == 0) {
+    if (elect_one()) {
       bool ok = true;
       for (int kt = kt0, it = 0; kt < kt1; ++kt, ++it) {
         const int s = it % S;
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer (each CTA its own halves)
-    if (lane == 0) {
+    if (elect_one()) {
       bool ok = true;
       uint32_t it = 0;
       pdl_wait();
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------ scale copies and MMAs (the even CTA's, for both)
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       bool ok = true;
       uint32_t it = 0, n = 0;
       for (int64_t t = pair; t < tiles && ok; t += pairs, ++n) {
@@ -528,51 +528,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < NT / cols; ++i) {
         const int c0 = b == 0 && C::kShared > 0 ? NT - (i + 1) * cols : i * cols;
         uint8_t* dst = buf + (stores % C::kBufs) * C::kWarpBuf;
+        uint32_t v[64];
+        uint32_t(&v0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[0]);
+        uint32_t(&v1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[32]);
+        tmem_ld_32x32b_x32(acc + c0, v0);
+        if (cols == 64) tmem_ld_32x32b_x32(acc + c0 + 32, v1);
+        tmem_ld_wait();
+        const bool shared_read = C::kShared > 0 && (i + 1) * cols == (C::kShared + cols - 1) / cols * cols;
+        if (shared_read || i + 1 == NT / cols) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (shared_read) mbar_arrive_remote_release(map_to_rank(&acc_shared[b], 0));
+            if (i + 1 == NT / cols) mbar_arrive_remote_release(map_to_rank(&acc_empty[b], 0));
+          }
+        }
         // the store that last used this buffer has read it
         if (lane == 0) bulk_wait_read<C::kBufs - 1>();
         __syncwarp();
-        uint32_t v[32];
         // 16-byte chunk c of row r lies at chunk c ^ (r & 7): the TMA map's swizzle
         uint8_t* line = dst + lane * 128;
         if (a.out_t == DBF_F32) {
-          tmem_ld_32x32b_x32(acc + c0, v);
-          tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             *reinterpret_cast<uint4*>(line + ((j ^ (lane & 7)) << 4)) =
                 make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         } else {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            tmem_ld_32x32b_x32(acc + c0 + 32 * h, v);
-            tmem_ld_wait();
+          for (int j = 0; j < 8; ++j) {
+            uint32_t w[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float lo = __uint_as_float(v[8 * j + 2 * e]), hi = __uint_as_float(v[8 * j + 2 * e + 1]);
-                if (a.out_t == DBF_F16) {
-                  const __half2 p2 = __floats2half2_rn(lo, hi);
-                  w[e] = *reinterpret_cast<const uint32_t*>(&p2);
-                } else {
-                  const __nv_bfloat162 p2 = __floats2bfloat162_rn(lo, hi);
-                  w[e] = *reinterpret_cast<const uint32_t*>(&p2);
-                }
+            for (int e = 0; e < 4; ++e) {
+              const float lo = __uint_as_float(v[8 * j + 2 * e]), hi = __uint_as_float(v[8 * j + 2 * e + 1]);
+              if (a.out_t == DBF_F16) {
+                const __half2 p2 = __floats2half2_rn(lo, hi);
+                w[e] = *reinterpret_cast<const uint32_t*>(&p2);
+              } else {
+                const __nv_bfloat162 p2 = __floats2bfloat162_rn(lo, hi);
+                w[e] = *reinterpret_cast<const uint32_t*>(&p2);
               }
-              *reinterpret_cast<uint4*>(line + (((4 * h + j) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
+            *reinterpret_cast<uint4*>(line + ((j ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
-        }
-        if (C::kShared > 0 && (i + 1) * cols == (C::kShared + cols - 1) / cols * cols) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote_release(map_to_rank(&acc_shared[b], 0));
-        }
-        if (i + 1 == NT / cols) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote_release(map_to_rank(&acc_empty[b], 0));
         }
         if (a.tma_out) {
           fence_proxy_async_smem();
