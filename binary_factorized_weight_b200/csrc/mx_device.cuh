@@ -111,7 +111,7 @@ __device__ __forceinline__ void mx_decode_e4m3(uint2 w, float (&v)[8]) {
   v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y, v[4] = c.x, v[5] = c.y, v[6] = d.x, v[7] = d.y;
 }
 
-// ---------------------------------------------------------------- eight elements of a row
+// ---------------------------------------------------------------- sixteen elements of a row
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(float v) { return v; }
@@ -130,94 +130,125 @@ __device__ __forceinline__ float from_f32<float>(float v) {
   return v;
 }
 
-// Eight elements as they lie in memory.
+// Sixteen elements as they lie in memory: what a thread holds of a row.
+constexpr int kChunk = 16;
 template <typename T>
-struct alignas(16) Pack8 {
-  T e[8];
+struct alignas(32) Pack16 {
+  T e[kChunk];
 };
 
-// Elements i .. i+7 of a row of `cols`; those behind the end read as zero.
-// VEC: i + 8 <= cols wherever i < cols, and the row starts on 16 bytes.
+// 32-byte accesses (global memory, 32-byte aligned).
+__device__ __forceinline__ void ldg_32(const void* p, uint32_t* r) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void stg_32(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// Elements 16 c .. 16 c + 15 of a row of `cols` (c consecutive over the warp's
+// lanes); those behind the end read as zero and are not written.
+// VEC: cols is a multiple of 16 and the row starts on 32 bytes.  Else the warp's
+// 512 columns pass through its 512 elements of shared memory, so that
+// neighbouring lanes touch neighbouring elements in memory.
 template <bool VEC, typename T>
-__device__ __forceinline__ Pack8<T> load8(const T* row, int64_t i, int64_t cols) {
-  Pack8<T> p;
+__device__ __forceinline__ Pack16<T> load16(const T* row, int64_t c, int64_t cols, T* stage) {
+  Pack16<T> p;
   if constexpr (VEC) {
-    if (i < cols) {
-      const uint4* src = reinterpret_cast<const uint4*>(row + i);
-      uint4* dst = reinterpret_cast<uint4*>(&p);
+    uint32_t* r = reinterpret_cast<uint32_t*>(&p);
+    if (kChunk * c < cols) {
 #pragma unroll
-      for (int j = 0; j < static_cast<int>(sizeof(p) / 16); ++j) dst[j] = src[j];
+      for (int j = 0; j < static_cast<int>(sizeof(p) / 32); ++j) ldg_32(row + kChunk * c + j * (32 / sizeof(T)), r + 8 * j);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) p.e[j] = from_f32<T>(0.f);
+      for (int j = 0; j < static_cast<int>(sizeof(p) / 4); ++j) r[j] = 0u;
     }
   } else {
+    const int lane = threadIdx.x & 31;
+    const int64_t first = kChunk * (c - lane) + lane;
+    T v[kChunk];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) p.e[j] = i + j < cols ? row[i + j] : from_f32<T>(0.f);
+    for (int j = 0; j < kChunk; ++j) v[j] = first + 32 * j < cols ? row[first + 32 * j] : from_f32<T>(0.f);
+    __syncwarp();  // earlier readers of the stage
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) stage[32 * j + lane] = v[j];
+    __syncwarp();
+    const uint4* src = reinterpret_cast<const uint4*>(stage + kChunk * lane);
+    uint4* dst = reinterpret_cast<uint4*>(&p);
+#pragma unroll
+    for (int j = 0; j < static_cast<int>(sizeof(p) / 16); ++j) dst[j] = src[j];
   }
   return p;
 }
 
 template <bool VEC, typename T>
-__device__ __forceinline__ void store8(T* row, int64_t i, int64_t cols, const Pack8<T>& p) {
+__device__ __forceinline__ void store16(T* row, int64_t c, int64_t cols, const Pack16<T>& p, T* stage) {
   if constexpr (VEC) {
-    if (i < cols) {
-      uint4* dst = reinterpret_cast<uint4*>(row + i);
-      const uint4* src = reinterpret_cast<const uint4*>(&p);
+    if (kChunk * c < cols) {
+      const uint32_t* r = reinterpret_cast<const uint32_t*>(&p);
 #pragma unroll
-      for (int j = 0; j < static_cast<int>(sizeof(p) / 16); ++j) dst[j] = src[j];
+      for (int j = 0; j < static_cast<int>(sizeof(p) / 32); ++j) stg_32(row + kChunk * c + j * (32 / sizeof(T)), r + 8 * j);
     }
   } else {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+    uint4* dst = reinterpret_cast<uint4*>(stage + kChunk * lane);
+    const uint4* src = reinterpret_cast<const uint4*>(&p);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (i + j < cols) row[i + j] = p.e[j];
+    for (int j = 0; j < static_cast<int>(sizeof(p) / 16); ++j) dst[j] = src[j];
+    __syncwarp();
+    const int64_t first = kChunk * (c - lane) + lane;
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j)
+      if (first + 32 * j < cols) row[first + 32 * j] = stage[32 * j + lane];
   }
 }
 
-// A warp's 256 neighbouring columns of one row -> codes and scales: lane l holds
-// columns 8 l .. 8 l + 7, a block is four neighbouring lanes, a scale word
-// sixteen.  c = column / 8 of this lane; nothing is written from pitch on
-// (pitch: the padded row length, a multiple of 128).
+// max(|a|, |b|, |c|), NaN if one of them is.
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// A warp's 512 neighbouring columns of one row -> codes and scales: the lane of
+// chunk c holds columns 16 c .., a block is two neighbouring lanes, a scale word
+// eight.  Nothing is written from pitch on (pitch: the padded row length, a
+// multiple of 128).
 template <int FMT>
-__device__ __forceinline__ void mx_store_row8(const float (&v)[8], int64_t r, int64_t c, int64_t pitch,
-                                              uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-  uint32_t amax = 0;
+__device__ __forceinline__ void mx_store_row16(const float (&v)[kChunk], int64_t r, int64_t c, int64_t pitch,
+                                               uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  float m = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  for (int j = 0; j < kChunk; j += 2) m = max_abs3(m, v[j], v[j + 1]);
+  uint32_t amax = __float_as_uint(m) & 0x7FFFFFFFu;
   amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
   const uint32_t byte = mx_scale_byte<FMT>(amax);
   const int lane = threadIdx.x & 31;
-  uint32_t word = byte << (8 * ((lane >> 2) & 3));
+  uint32_t word = byte << (8 * ((lane >> 1) & 3));
+  word |= __shfl_xor_sync(0xffffffffu, word, 2);
   word |= __shfl_xor_sync(0xffffffffu, word, 4);
-  word |= __shfl_xor_sync(0xffffffffu, word, 8);
-  float u[8];
+  if (kChunk * c >= pitch) return;
+  const bool bad = byte == 255;
   const float inv = mx_inverse_scale(min(byte, 253u));
+  float u[kChunk];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) u[j] = byte == 255 ? 0.f : v[j] * inv;
-  if (8 * c >= pitch) return;
+  for (int j = 0; j < kChunk; ++j) u[j] = v[j] * inv;
+  const float(&lo)[8] = *reinterpret_cast<const float(*)[8]>(&u[0]);
+  const float(&hi)[8] = *reinterpret_cast<const float(*)[8]>(&u[8]);
   if constexpr (FMT == kMx4) {
-    *reinterpret_cast<uint32_t*>(codes + (r * pitch >> 1) + 4 * c) = mx_encode_e2m1(u);
+    const uint2 q = make_uint2(mx_encode_e2m1(lo), mx_encode_e2m1(hi));
+    *reinterpret_cast<uint2*>(codes + (r * pitch >> 1) + 8 * c) = bad ? make_uint2(0u, 0u) : q;
   } else {
-    *reinterpret_cast<uint2*>(codes + r * pitch + 8 * c) =
-        make_uint2(mx_encode_e4m3(u[0], u[1], u[2], u[3]), mx_encode_e4m3(u[4], u[5], u[6], u[7]));
+    const uint4 q = make_uint4(mx_encode_e4m3(u[0], u[1], u[2], u[3]), mx_encode_e4m3(u[4], u[5], u[6], u[7]),
+                               mx_encode_e4m3(u[8], u[9], u[10], u[11]), mx_encode_e4m3(u[12], u[13], u[14], u[15]));
+    *reinterpret_cast<uint4*>(codes + r * pitch + 16 * c) = bad ? make_uint4(0u, 0u, 0u, 0u) : q;
   }
-  if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(scales + mx_scale_word(r, c >> 4, pitch >> 7)) = word;
-}
-
-// Sum of one value per thread over the block (every thread gets it).  `red`:
-// 33 floats of shared memory, free to be reused after the next __syncthreads.
-__device__ __forceinline__ float block_sum(float v, float* red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  if (warps == 1) return v;
-  if (lane == 0) red[warp] = v;
-  __syncthreads();
-  float s = lane < warps ? red[lane] : 0.f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
+  if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(scales + mx_scale_word(r, c >> 3, pitch >> 7)) = word;
 }
 
 }  // namespace dbf

@@ -14,92 +14,131 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// One warp item: 256 neighbouring columns of one row, eight per lane.
+// it / n for the items of one launch: in 32 bits where they fit (a 64-bit
+// division costs as much as the rest of an item).
+__device__ __forceinline__ int64_t row_of(int64_t it, uint32_t n, bool small) {
+  return small ? static_cast<int64_t>(static_cast<uint32_t>(it) / n) : it / n;
+}
+
+// One warp item: 512 neighbouring columns of one row, sixteen per lane (32
+// bytes of 16-bit elements in one access).
 template <typename T, int FMT, bool VEC>
 __global__ void __launch_bounds__(kThreads) dbf_mx_quantize_kernel(const T* __restrict__ src, int64_t rows,
                                                                    int64_t cols, int64_t pitch,
                                                                    uint8_t* __restrict__ codes,
                                                                    uint8_t* __restrict__ scales) {
+  __shared__ alignas(32) T stage[VEC ? 1 : kThreads * kChunk];
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t per_row = (pitch + 255) >> 8;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t per_row = static_cast<uint32_t>((pitch + 511) >> 9);
   const int64_t items = rows * per_row;
+  const bool small = items <= 0xffffffffll;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); it < items; it += step) {
-    const int64_t r = it / per_row;
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + warp; it < items; it += step) {
+    const int64_t r = row_of(it, per_row, small);
     const int64_t c = (it - r * per_row) * 32 + lane;
-    const Pack8<T> p = load8<VEC>(src + r * cols, 8 * c, cols);
-    float v[8];
+    const Pack16<T> p = load16<VEC>(src + r * cols, c, cols, stage + (VEC ? 0 : warp * 32 * kChunk));
+    float v[kChunk];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = to_f32(p.e[j]);
-    mx_store_row8<FMT>(v, r, c, pitch, codes, scales);
+    for (int j = 0; j < kChunk; ++j) v[j] = to_f32(p.e[j]);
+    mx_store_row16<FMT>(v, r, c, pitch, codes, scales);
   }
 }
 
 // The transpose: output row = source column, blocks of 32 run down the source's
-// rows.  A CTA takes 128 source rows x 64 source columns through shared memory
-// (fp32); thread (column, block) then holds a whole block of 32 values.  The
-// four blocks of a column are neighbouring lanes: their codes are one
-// contiguous run and their scale bytes one word.  Each 32-row block is shifted
-// by 8 words in shared memory, so the warp's 4 blocks x 8 columns of one read
-// lie in 32 banks.
-constexpr int kTRows = 128, kTCols = 64, kTLd = kTCols + 1;
-template <typename T, int FMT>
-__global__ void __launch_bounds__(kThreads) dbf_mx_quantize_t_kernel(const T* __restrict__ src, int64_t rows,
-                                                                     int64_t cols, int64_t pitch,
-                                                                     uint8_t* __restrict__ codes,
-                                                                     uint8_t* __restrict__ scales) {
-  __shared__ float tile[kTRows * kTLd + 3 * 8];
+// rows.  A CTA takes 128 source rows x 128 (fp32: 64) source columns through
+// shared memory; a thread then holds two neighbouring columns' blocks of 32
+// (each read of shared memory brings both).  The four blocks of a column are
+// neighbouring lanes: their codes are one contiguous run and their scale bytes
+// one word.  Each 32-row block is shifted by 8 words, so a warp's read of 4
+// blocks x 8 column pairs lies in 32 banks.
+constexpr int kTRows = 128;
+template <typename T>
+constexpr int kTCols = sizeof(T) == 2 ? 128 : 64;
+template <typename T>
+constexpr int kTThreads = 2 * kTCols<T>;
+
+template <typename T>
+struct alignas(2 * sizeof(T)) Pair {
+  T a, b;
+};
+
+template <int FMT>
+__device__ __forceinline__ void mx_store_block(const float (&v)[32], int64_t r, int64_t k4, int blk, int64_t pitch,
+                                               bool valid, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) m = max_abs3(m, v[j], v[j + 1]);
+  const uint32_t byte = mx_scale_byte<FMT>(__float_as_uint(m) & 0x7FFFFFFFu);
+  uint32_t word = byte << (8 * blk);
+  word |= __shfl_xor_sync(0xffffffffu, word, 1);
+  word |= __shfl_xor_sync(0xffffffffu, word, 2);
+  if (!valid) return;
+  const float inv = mx_inverse_scale(min(byte, 253u));
+  uint32_t q[FMT == kMx4 ? 4 : 8];
+#pragma unroll
+  for (int j = 0; j < 32; j += 8) {
+    float u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = v[j + i] * inv;
+    if constexpr (FMT == kMx4) {
+      q[j / 8] = byte == 255 ? 0u : mx_encode_e2m1(u);
+    } else {
+      q[j / 4] = byte == 255 ? 0u : mx_encode_e4m3(u[0], u[1], u[2], u[3]);
+      q[j / 4 + 1] = byte == 255 ? 0u : mx_encode_e4m3(u[4], u[5], u[6], u[7]);
+    }
+  }
+  const int64_t at = r * pitch + k4 * 128 + blk * 32;
+  uint4* dst = reinterpret_cast<uint4*>(codes + (FMT == kMx4 ? at >> 1 : at));
+  dst[0] = make_uint4(q[0], q[1], q[2], q[3]);
+  if constexpr (FMT == kMx8) dst[1] = make_uint4(q[4], q[5], q[6], q[7]);
+  if (blk == 0) *reinterpret_cast<uint32_t*>(scales + mx_scale_word(r, k4, pitch >> 7)) = word;
+}
+
+template <typename T, int FMT, bool VEC>
+__global__ void __launch_bounds__(kTThreads<T>) dbf_mx_quantize_t_kernel(const T* __restrict__ src, int64_t rows,
+                                                                         int64_t cols, int64_t pitch,
+                                                                         uint8_t* __restrict__ codes,
+                                                                         uint8_t* __restrict__ scales) {
+  constexpr int kCols = kTCols<T>, kPad = 32 / sizeof(T), kVec = 16 / sizeof(T);
+  __shared__ alignas(16) T tile[kTRows * kCols + 3 * kPad];
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t col_tiles = (cols + kTCols - 1) / kTCols;
+  const int64_t col_tiles = (cols + kCols - 1) / kCols;
   const int64_t items = col_tiles * (pitch >> 7);
   const int tid = threadIdx.x;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const int64_t k4 = it / col_tiles;  // 128 source rows
-    const int64_t c0 = (it - k4 * col_tiles) * kTCols;
-    for (int i = tid; i < kTRows * kTCols; i += kThreads) {
-      const int rr = i / kTCols, cc = i % kTCols;
-      const int64_t r = k4 * kTRows + rr, c = c0 + cc;
-      tile[rr * kTLd + (rr >> 5) * 8 + cc] = r < rows && c < cols ? to_f32(src[r * cols + c]) : 0.f;
-    }
-    __syncthreads();
-    const int blk = tid & 3, cc = tid >> 2;
-    const float* base = tile + blk * (32 * kTLd + 8) + cc;
-    float v[32];
-    uint32_t amax = 0;
+    const int64_t c0 = (it - k4 * col_tiles) * kCols;
+    if constexpr (VEC) {  // cols a multiple of 16 bytes: whole vectors lie inside or outside
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      v[j] = base[j * kTLd];
-      amax = max(amax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-    }
-    const uint32_t byte = mx_scale_byte<FMT>(amax);
-    uint32_t word = byte << (8 * blk);
-    word |= __shfl_xor_sync(0xffffffffu, word, 1);
-    word |= __shfl_xor_sync(0xffffffffu, word, 2);
-    const float inv = mx_inverse_scale(min(byte, 253u));
-    uint32_t q[FMT == kMx4 ? 4 : 8];
-#pragma unroll
-    for (int j = 0; j < 32; j += 8) {
-      float u[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] = byte == 255 ? 0.f : v[j + i] * inv;
-      if constexpr (FMT == kMx4) {
-        q[j / 8] = mx_encode_e2m1(u);
-      } else {
-        q[j / 4] = mx_encode_e4m3(u[0], u[1], u[2], u[3]);
-        q[j / 4 + 1] = mx_encode_e4m3(u[4], u[5], u[6], u[7]);
+      for (int i = 0; i < kTRows * kCols / kVec / kTThreads<T>; ++i) {
+        const int at = i * kTThreads<T> + tid, rr = at / (kCols / kVec), cc = at % (kCols / kVec) * kVec;
+        const int64_t r = k4 * kTRows + rr, c = c0 + cc;
+        const uint4 v = r < rows && c < cols ? *reinterpret_cast<const uint4*>(src + r * cols + c) : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(&tile[rr * kCols + (rr >> 5) * kPad + cc]) = v;
+      }
+    } else {
+      for (int i = tid; i < kTRows * kCols; i += kTThreads<T>) {
+        const int rr = i / kCols, cc = i % kCols;
+        const int64_t r = k4 * kTRows + rr, c = c0 + cc;
+        tile[rr * kCols + (rr >> 5) * kPad + cc] = r < rows && c < cols ? src[r * cols + c] : from_f32<T>(0.f);
       }
     }
-    const int64_t r = c0 + cc;  // output row
-    if (r < cols) {
-      const int64_t at = r * pitch + k4 * 128 + blk * 32;
-      uint4* dst = reinterpret_cast<uint4*>(codes + (FMT == kMx4 ? at >> 1 : at));
-      dst[0] = make_uint4(q[0], q[1], q[2], q[3]);
-      if constexpr (FMT == kMx8) dst[1] = make_uint4(q[4], q[5], q[6], q[7]);
-      if (blk == 0) *reinterpret_cast<uint32_t*>(scales + mx_scale_word(r, k4, pitch >> 7)) = word;
+    __syncthreads();
+    const int blk = tid & 3, cc = 2 * (tid >> 2);
+    const T* base = tile + blk * (32 * kCols + kPad) + cc;
+    float v[2][32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const Pair<T> t = *reinterpret_cast<const Pair<T>*>(base + j * kCols);
+      v[0][j] = to_f32(t.a);
+      v[1][j] = to_f32(t.b);
     }
+    const int64_t r = c0 + cc;  // output row
+    mx_store_block<FMT>(v[0], r, k4, blk, pitch, r < cols, codes, scales);
+    mx_store_block<FMT>(v[1], r + 1, k4, blk, pitch, r + 1 < cols, codes, scales);
     __syncthreads();
   }
 }
@@ -108,27 +147,34 @@ template <typename T, int FMT, bool VEC>
 __global__ void __launch_bounds__(kThreads) dbf_mx_dequantize_kernel(const uint8_t* __restrict__ codes,
                                                                      const uint8_t* __restrict__ scales, int64_t rows,
                                                                      int64_t cols, int64_t pitch, T* __restrict__ dst) {
+  __shared__ alignas(32) T stage[VEC ? 1 : kThreads * kChunk];
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t per_row = (cols + 255) >> 8;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t per_row = static_cast<uint32_t>((cols + 511) >> 9);
   const int64_t items = rows * per_row;
+  const bool small = items <= 0xffffffffll;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); it < items; it += step) {
-    const int64_t r = it / per_row;
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + warp; it < items; it += step) {
+    const int64_t r = row_of(it, per_row, small);
     const int64_t c = (it - r * per_row) * 32 + lane;
-    if (8 * c >= cols) continue;
-    float v[8];
-    if constexpr (FMT == kMx4) {
-      mx_decode_e2m1(*reinterpret_cast<const uint32_t*>(codes + (r * pitch >> 1) + 4 * c), v);
-    } else {
-      mx_decode_e4m3(*reinterpret_cast<const uint2*>(codes + r * pitch + 8 * c), v);
-    }
-    const float s = mx_scale(scales[mx_scale_word(r, c >> 4, pitch >> 7) + ((c >> 2) & 3)]);
-    Pack8<T> p;
+    Pack16<T> p;
+    if (kChunk * c < cols) {
+      float v[2][8];
+      if constexpr (FMT == kMx4) {
+        const uint2 w = *reinterpret_cast<const uint2*>(codes + (r * pitch >> 1) + 8 * c);
+        mx_decode_e2m1(w.x, v[0]);
+        mx_decode_e2m1(w.y, v[1]);
+      } else {
+        const uint4 w = *reinterpret_cast<const uint4*>(codes + r * pitch + 16 * c);
+        mx_decode_e4m3(make_uint2(w.x, w.y), v[0]);
+        mx_decode_e4m3(make_uint2(w.z, w.w), v[1]);
+      }
+      const float s = mx_scale(scales[mx_scale_word(r, c >> 3, pitch >> 7) + ((c >> 1) & 3)]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) p.e[j] = from_f32<T>(v[j] * s);
-    store8<VEC>(dst + r * cols, 8 * c, cols, p);
+      for (int j = 0; j < kChunk; ++j) p.e[j] = from_f32<T>(v[j >> 3][j & 7] * s);
+    }
+    store16<VEC>(dst + r * cols, c, cols, p, stage + (VEC ? 0 : warp * 32 * kChunk));
   }
 }
 
@@ -142,13 +188,17 @@ dbf_status quantize_typed(const void* src, int64_t rows, int64_t cols, bool tran
   const T* s = static_cast<const T*>(src);
   if (transpose) {
     const int64_t pitch = mx_pitch(rows);
-    const int64_t items = (cols + kTCols - 1) / kTCols * (pitch >> 7);
-    return launch_pdl(dbf_mx_quantize_t_kernel<T, FMT>, dim3(grid_for(items, 1, dev)), dim3(kThreads), 0, stream, s,
-                      rows, cols, pitch, codes, scales);
+    const int64_t items = (cols + kTCols<T> - 1) / kTCols<T> * (pitch >> 7);
+    const dim3 grid(grid_for(items, 1, dev)), block(kTThreads<T>);
+    return cols * sizeof(T) % 16 == 0 && aligned_to(src, 16)
+               ? launch_pdl(dbf_mx_quantize_t_kernel<T, FMT, true>, grid, block, 0, stream, s, rows, cols, pitch, codes,
+                            scales)
+               : launch_pdl(dbf_mx_quantize_t_kernel<T, FMT, false>, grid, block, 0, stream, s, rows, cols, pitch, codes,
+                            scales);
   }
   const int64_t pitch = mx_pitch(cols);
-  const int64_t items = rows * ((pitch + 255) >> 8);
-  const bool vec = cols % 8 == 0 && aligned_to(src, 16);
+  const int64_t items = rows * ((pitch + 511) >> 9);
+  const bool vec = cols % kChunk == 0 && aligned_to(src, 32);
   const dim3 grid(grid_for(items, kThreads / 32, dev));
   return vec ? launch_pdl(dbf_mx_quantize_kernel<T, FMT, true>, grid, dim3(kThreads), 0, stream, s, rows, cols, pitch,
                           codes, scales)
@@ -161,9 +211,9 @@ dbf_status dequantize_typed(const uint8_t* codes, const uint8_t* scales, int64_t
                             const DeviceInfo& dev, cudaStream_t stream) {
   T* d = static_cast<T*>(dst);
   const int64_t pitch = mx_pitch(cols);
-  const int64_t items = rows * ((cols + 255) >> 8);
+  const int64_t items = rows * ((cols + 511) >> 9);
   const dim3 grid(grid_for(items, kThreads / 32, dev));
-  const bool vec = cols % 8 == 0 && aligned_to(dst, 16);
+  const bool vec = cols % kChunk == 0 && aligned_to(dst, 32);
   return vec ? launch_pdl(dbf_mx_dequantize_kernel<T, FMT, true>, grid, dim3(kThreads), 0, stream, codes, scales, rows,
                           cols, pitch, d)
              : launch_pdl(dbf_mx_dequantize_kernel<T, FMT, false>, grid, dim3(kThreads), 0, stream, codes, scales, rows,

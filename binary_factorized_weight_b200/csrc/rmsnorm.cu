@@ -8,6 +8,7 @@
 // The sums are fp32.  Every operand is read once where a row fits the block's
 // registers, so DRAM bounds all of it; few rows are bound by latency.
 #include <algorithm>
+#include <mutex>
 
 #include "dbf_internal.h"
 #include "mx_device.cuh"
@@ -29,93 +30,129 @@ struct NormArgs {
   float eps;
 };
 
-// One block per row (persistent over rows); thread t owns the eight columns of
-// chunks t, t + threads, .. (NV of them, held in registers).  NV = 0: any
-// number of chunks, the second pass reads h (or x) again.
-template <typename T, int OUT, int NV, bool VEC>
-__global__ void __launch_bounds__(1024) dbf_rmsnorm_kernel(const NormArgs p) {
-  __shared__ float red[2][33];
+// Sum of one value per thread over the row's threads (every thread gets it):
+// the warp's where a row is a warp's work, else the block's.  `red`: 32 floats
+// of shared memory, free to be reused two calls later.
+template <bool WARP>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (WARP) return v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  float s = lane < warps ? red[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+constexpr int kWarpRows = 8;          // rows of a block whose warps take a row each
+constexpr int kStagedThreads = 512;   // threads of a block that stages its rows in shared memory, at most
+
+// A row is the work of one warp (WARP: up to 1024 columns, eight rows to a
+// block) or of a block; persistent over rows.  Thread t of the row owns the
+// sixteen columns of chunks t, t + threads, .. (NV of them, held in registers,
+// so everything is read once).  NV = 0: any number of chunks, the second pass
+// reads h (or x) again.
+template <typename T, int OUT, int NV, bool VEC, bool WARP>
+__global__ void __launch_bounds__(VEC && !WARP ? 1024 : kStagedThreads) dbf_rmsnorm_kernel(const NormArgs p) {
+  __shared__ float red[2][32];
+  __shared__ alignas(32) T stages[VEC ? 1 : (WARP ? 32 * kWarpRows : kStagedThreads) * kChunk];
   pdl_wait();
   pdl_launch_dependents();
   const T* x = static_cast<const T*>(p.x);
   const T* res = static_cast<const T*>(p.residual);
   const T* weight = static_cast<const T*>(p.weight);
-  const int64_t chunks = p.pitch >> 3;
+  T* stage = stages + (VEC ? 0 : (threadIdx.x >> 5) * 32 * kChunk);
+  const int me = WARP ? threadIdx.x & 31 : threadIdx.x, threads = WARP ? 32 : blockDim.x;
+  const int64_t row_step = static_cast<int64_t>(gridDim.x) * (WARP ? kWarpRows : 1);
+  const float inv_cols = 1.f / static_cast<float>(p.cols);
   int flip = 0;
-  for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x, flip ^= 1) {
+  for (int64_t r = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x; r < p.rows;
+       r += row_step, flip ^= 1) {
     const T* xr = x + r * p.cols;
     const T* rr = res ? res + r * p.cols : nullptr;
     T* hr = res ? static_cast<T*>(p.h) + r * p.cols : nullptr;
     float sum = 0.f;
     auto fetch = [&](int64_t c) {
-      Pack8<T> a = load8<VEC>(xr, 8 * c, p.cols);
+      Pack16<T> a = load16<VEC>(xr, c, p.cols, stage);
       if (rr) {
-        const Pack8<T> b = load8<VEC>(rr, 8 * c, p.cols);
+        const Pack16<T> b = load16<VEC>(rr, c, p.cols, stage);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a.e[j] = from_f32<T>(to_f32(a.e[j]) + to_f32(b.e[j]));
-        store8<VEC>(hr, 8 * c, p.cols, a);
+        for (int j = 0; j < kChunk; ++j) a.e[j] = from_f32<T>(to_f32(a.e[j]) + to_f32(b.e[j]));
+        store16<VEC>(hr, c, p.cols, a, stage);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum = fmaf(to_f32(a.e[j]), to_f32(a.e[j]), sum);
+      for (int j = 0; j < kChunk; ++j) sum = fmaf(to_f32(a.e[j]), to_f32(a.e[j]), sum);
       return a;
     };
-    auto finish = [&](int64_t c, const Pack8<T>& a, const Pack8<T>& w, float rstd) {
-      float v[8];
+    auto finish = [&](int64_t c, const Pack16<T>& a, const Pack16<T>& w, float rstd) {
+      float v[kChunk];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = to_f32(a.e[j]) * rstd * to_f32(w.e[j]);
+      for (int j = 0; j < kChunk; ++j) v[j] = to_f32(a.e[j]) * rstd * to_f32(w.e[j]);
       if constexpr (OUT == kDense) {
-        Pack8<T> o;
+        Pack16<T> o;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o.e[j] = from_f32<T>(v[j]);
-        store8<VEC>(static_cast<T*>(p.y) + r * p.cols, 8 * c, p.cols, o);
+        for (int j = 0; j < kChunk; ++j) o.e[j] = from_f32<T>(v[j]);
+        store16<VEC>(static_cast<T*>(p.y) + r * p.cols, c, p.cols, o, stage);
       } else {
-        mx_store_row8<OUT>(v, r, c, p.pitch, p.codes, p.scales);
+        mx_store_row16<OUT>(v, r, c, p.pitch, p.codes, p.scales);
       }
     };
-    const float inv_cols = 1.f / static_cast<float>(p.cols);
     if constexpr (NV > 0) {
-      Pack8<T> a[NV], w[NV];
+      Pack16<T> a[NV], w[NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int64_t c = threadIdx.x + static_cast<int64_t>(i) * blockDim.x;
+        const int64_t c = me + i * threads;
         a[i] = fetch(c);
-        w[i] = load8<VEC>(weight, 8 * c, p.cols);
+        w[i] = load16<VEC>(weight, c, p.cols, stage);
       }
-      const float rstd = 1.f / sqrtf(block_sum(sum, red[flip]) * inv_cols + p.eps);
+      const float rstd = 1.f / sqrtf(row_sum<WARP>(sum, red[flip]) * inv_cols + p.eps);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) finish(threadIdx.x + static_cast<int64_t>(i) * blockDim.x, a[i], w[i], rstd);
+      for (int i = 0; i < NV; ++i) finish(me + i * threads, a[i], w[i], rstd);
     } else {
-      // a whole number of rounds for every thread: the MX store is a warp's work
-      const int64_t rounds = (chunks + blockDim.x - 1) / blockDim.x;
-      for (int64_t i = 0; i < rounds; ++i) fetch(threadIdx.x + i * blockDim.x);
-      const float rstd = 1.f / sqrtf(block_sum(sum, red[flip]) * inv_cols + p.eps);
+      // a whole number of rounds for every thread: staging and the MX store are a warp's work
+      const int64_t rounds = ((p.pitch + kChunk - 1) / kChunk + threads - 1) / threads;
+      for (int64_t i = 0; i < rounds; ++i) fetch(me + i * threads);
+      const float rstd = 1.f / sqrtf(row_sum<WARP>(sum, red[flip]) * inv_cols + p.eps);
       const T* again = rr ? hr : xr;
       for (int64_t i = 0; i < rounds; ++i) {
-        const int64_t c = threadIdx.x + i * blockDim.x;
-        finish(c, load8<VEC>(again, 8 * c, p.cols), load8<VEC>(weight, 8 * c, p.cols), rstd);
+        const int64_t c = me + i * threads;
+        finish(c, load16<VEC>(again, c, p.cols, stage), load16<VEC>(weight, c, p.cols, stage), rstd);
       }
     }
   }
 }
 
+// With few rows (less than one to an SM) a row gets as many threads as it has
+// chunks; else up to 1024 columns are one warp's work.
 template <typename T, int OUT, bool VEC>
 dbf_status launch_norm(const NormArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
-  const int64_t chunks = (a.pitch + 7) / 8;
-  const int nv = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 0;
-  const int64_t want = nv ? (chunks + nv - 1) / nv : 1024;
+  const int64_t chunks = (a.pitch + kChunk - 1) / kChunk;
+  if (chunks <= 64 && (chunks <= 32 || a.rows >= dev.num_sms)) {
+    const dim3 grid(static_cast<unsigned>(
+        std::min<int64_t>((a.rows + kWarpRows - 1) / kWarpRows, int64_t{dev.num_sms} * 8)));
+    const dim3 block(32 * kWarpRows);
+    if (chunks <= 32) return launch_pdl(dbf_rmsnorm_kernel<T, OUT, 1, VEC, true>, grid, block, 0, stream, a);
+    return launch_pdl(dbf_rmsnorm_kernel<T, OUT, 2, VEC, true>, grid, block, 0, stream, a);
+  }
+  const int most = VEC ? 1024 : kStagedThreads;
+  const int nv = chunks <= most ? 1 : chunks <= 2 * most ? 2 : 0;
+  const int64_t want = nv ? (chunks + nv - 1) / nv : most;
   const int threads = static_cast<int>((want + 31) / 32 * 32);
-  const int per_sm = std::max(1, 2048 / threads);
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t{dev.num_sms} * std::min(per_sm, 16))));
+  const dim3 grid(
+      static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t{dev.num_sms} * std::min(std::max(1, 2048 / threads), 16))));
   const dim3 block(threads);
-  if (nv == 1) return launch_pdl(dbf_rmsnorm_kernel<T, OUT, 1, VEC>, grid, block, 0, stream, a);
-  if (nv == 2) return launch_pdl(dbf_rmsnorm_kernel<T, OUT, 2, VEC>, grid, block, 0, stream, a);
-  return launch_pdl(dbf_rmsnorm_kernel<T, OUT, 0, VEC>, grid, block, 0, stream, a);
+  if (nv == 1) return launch_pdl(dbf_rmsnorm_kernel<T, OUT, 1, VEC, false>, grid, block, 0, stream, a);
+  if (nv == 2) return launch_pdl(dbf_rmsnorm_kernel<T, OUT, 2, VEC, false>, grid, block, 0, stream, a);
+  return launch_pdl(dbf_rmsnorm_kernel<T, OUT, 0, VEC, false>, grid, block, 0, stream, a);
 }
 
 template <typename T, int OUT>
 dbf_status norm_typed(const NormArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
-  const bool vec = a.cols % 8 == 0 && aligned_to(a.x, 16) && aligned_to(a.residual, 16) && aligned_to(a.weight, 16) &&
-                   aligned_to(a.h, 16) && aligned_to(a.y, 16);
+  const bool vec = a.cols % kChunk == 0 && aligned_to(a.x, 32) && aligned_to(a.residual, 32) &&
+                   aligned_to(a.weight, 32) && aligned_to(a.h, 32) && aligned_to(a.y, 32);
   return vec ? launch_norm<T, OUT, true>(a, dev, stream) : launch_norm<T, OUT, false>(a, dev, stream);
 }
 
@@ -140,21 +177,22 @@ struct NormGradArgs {
   float eps;
 };
 
-// Sums of two values per thread over the block; red: 66 floats.
-__device__ __forceinline__ float2 block_sum2(float a, float b, float* red) {
+// Sums of two values per thread over the row's threads; red: 64 floats.
+template <bool WARP>
+__device__ __forceinline__ float2 row_sum2(float a, float b, float* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     a += __shfl_xor_sync(0xffffffffu, a, o);
     b += __shfl_xor_sync(0xffffffffu, b, o);
   }
+  if (WARP) return make_float2(a, b);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  if (warps == 1) return make_float2(a, b);
   if (lane == 0) {
     red[warp] = a;
-    red[33 + warp] = b;
+    red[32 + warp] = b;
   }
   __syncthreads();
-  float s = lane < warps ? red[lane] : 0.f, t = lane < warps ? red[33 + lane] : 0.f;
+  float s = lane < warps ? red[lane] : 0.f, t = lane < warps ? red[32 + lane] : 0.f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -163,56 +201,158 @@ __device__ __forceinline__ float2 block_sum2(float a, float b, float* red) {
   return make_float2(s, t);
 }
 
-// One block per row at a time, eight columns per thread (cols <= 8192); the
-// block's sum of dweight over its rows stays in registers and goes to its row
-// of `part`.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(1024) dbf_rmsnorm_grad_kernel(const NormGradArgs p) {
-  __shared__ float red[2][66];
-  pdl_wait();
-  pdl_launch_dependents();
-  const int64_t i = 8 * static_cast<int64_t>(threadIdx.x);
-  const Pack8<T> w = load8<VEC>(static_cast<const T*>(p.weight), i, p.cols);
-  const float inv_cols = 1.f / static_cast<float>(p.cols);
-  float dw[8] = {};
-  int flip = 0;
-  for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x, flip ^= 1) {
-    const Pack8<T> h = load8<VEC>(static_cast<const T*>(p.h) + r * p.cols, i, p.cols);
-    const Pack8<T> dy = load8<VEC>(static_cast<const T*>(p.dy) + r * p.cols, i, p.cols);
-    Pack8<T> dh;
-    if (p.dh) dh = load8<VEC>(static_cast<const T*>(p.dh) + r * p.cols, i, p.cols);
-    float hh = 0.f, gh = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = to_f32(h.e[j]);
-      hh = fmaf(a, a, hh);
-      gh = fmaf(to_f32(dy.e[j]) * to_f32(w.e[j]), a, gh);
-    }
-    const float2 s = block_sum2(hh, gh, red[flip]);
-    const float rstd = 1.f / sqrtf(s.x * inv_cols + p.eps);
-    const float c = rstd * rstd * rstd * (s.y * inv_cols);
-    Pack8<T> o;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = to_f32(h.e[j]), d = to_f32(dy.e[j]);
-      float v = rstd * (d * to_f32(w.e[j])) - a * c;
-      if (p.dh) v += to_f32(dh.e[j]);
-      o.e[j] = from_f32<T>(v);
-      dw[j] = fmaf(d * a, rstd, dw[j]);
-    }
-    store8<VEC>(static_cast<T*>(p.dx) + r * p.cols, i, p.cols, o);
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (i + j < p.cols) p.part[blockIdx.x * p.cols + i + j] = dw[j];
+__device__ __forceinline__ void cp_async_16(void* smem_dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem_dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Rows wider than a block: the row's two sums first (from a first reading),
+// A row is the work of one warp (WARP, eight rows to a block) or of a block;
+// NV * 16 columns per thread, whose sums of dweight over the rows stay in
+// registers and go to the block's row of `part`.
+// VEC: a thread copies its own columns of the rows to come into shared memory
+// (cp.async), so loads are under way all the time and no thread waits for
+// another's; it owns sixteen neighbouring columns and reads them once for the
+// sums and once for the gradients.  Else it owns every threads-th column and
+// reads it where it is, the second time from L1.
+constexpr int kGradThreads = 512;
+// rows of the ring: as many as a block of kGradThreads has room for
+template <typename T, int NV, bool WARP>
+constexpr int kDepth = WARP || NV * sizeof(T) == 2 ? 3 : 2;
+template <typename T, int NV, bool VEC, bool WARP>
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kGradThreads, WARP ? 2 : 1)
+    dbf_rmsnorm_grad_kernel(const NormGradArgs p) {
+  constexpr int N = NV * kChunk, D = kDepth<T, NV, WARP>;
+  __shared__ float red[2][64];
+  extern __shared__ uint8_t ring[];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int me = WARP ? threadIdx.x & 31 : threadIdx.x, threads = WARP ? 32 : blockDim.x;
+  const int group = WARP ? threadIdx.x >> 5 : 0;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * (WARP ? kWarpRows : 1) + group;
+  const int64_t row_step = static_cast<int64_t>(gridDim.x) * (WARP ? kWarpRows : 1);
+  const T* src[3] = {static_cast<const T*>(p.h), static_cast<const T*>(p.dy), static_cast<const T*>(p.dh)};
+  const int operands = p.dh ? 3 : 2;
+  // column of this thread's element n
+  auto column = [&](int n) -> int64_t {
+    return VEC ? kChunk * (me + static_cast<int64_t>(n / kChunk) * threads) + n % kChunk
+               : me + static_cast<int64_t>(n) * threads;
+  };
+  const float inv_cols = 1.f / static_cast<float>(p.cols);
+  T w[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+    w[n] = column(n) < p.cols ? static_cast<const T*>(p.weight)[column(n)] : from_f32<T>(0.f);
+  // this thread's part of the ring: [stage][operand][NV] packs
+  Pack16<T>* mine = reinterpret_cast<Pack16<T>*>(ring) + static_cast<size_t>(threadIdx.x) * (D * 3 * NV);
+  auto prefetch = [&](int64_t r, int stage) {
+    if constexpr (VEC) {
+      if (r < p.rows) {
+        for (int o = 0; o < operands; ++o) {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            if (column(kChunk * i) < p.cols) {
+              const char* from = reinterpret_cast<const char*>(src[o] + r * p.cols + column(kChunk * i));
+              char* to = reinterpret_cast<char*>(mine + (stage * 3 + o) * NV + i);
+#pragma unroll
+              for (int b = 0; b < static_cast<int>(sizeof(Pack16<T>)); b += 16) cp_async_16(to + b, from + b);
+            }
+          }
+        }
+      }
+      cp_async_commit();
+    }
+  };
+  // sixteen of this thread's elements of an operand's row
+  auto fetch = [&](int o, int i, int64_t r, int stage) {
+    Pack16<T> a;
+    if constexpr (VEC) {
+      a = mine[(stage * 3 + o) * NV + i];
+      if (column(kChunk * i) >= p.cols) {
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) a.e[j] = from_f32<T>(0.f);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) {
+        const int64_t c = column(kChunk * i + j);
+        a.e[j] = c < p.cols ? src[o][r * p.cols + c] : from_f32<T>(0.f);
+      }
+    }
+    return a;
+  };
+  float dw[N] = {};
+  int flip = 0, stage = 0;
+#pragma unroll
+  for (int d = 0; d < D - 1; ++d) prefetch(row0 + d * row_step, d);
+  for (int64_t r = row0; r < p.rows; r += row_step, flip ^= 1, stage = stage + 1 == D ? 0 : stage + 1) {
+    prefetch(r + (D - 1) * row_step, stage == 0 ? D - 1 : stage - 1);
+    cp_async_wait<D - 1>();
+    float hh = 0.f, gh = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const Pack16<T> h = fetch(0, i, r, stage), dy = fetch(1, i, r, stage);
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) {
+        const float a = to_f32(h.e[j]);
+        hh = fmaf(a, a, hh);
+        gh = fmaf(to_f32(dy.e[j]) * to_f32(w[kChunk * i + j]), a, gh);
+      }
+    }
+    const float2 s = row_sum2<WARP>(hh, gh, red[flip]);
+    const float rstd = 1.f / sqrtf(s.x * inv_cols + p.eps);
+    const float c = rstd * rstd * rstd * (s.y * inv_cols);
+    T* dx = static_cast<T*>(p.dx) + r * p.cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const Pack16<T> h = fetch(0, i, r, stage), dy = fetch(1, i, r, stage);
+      Pack16<T> o;
+      if (p.dh) o = fetch(2, i, r, stage);
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) {
+        const int n = kChunk * i + j;
+        const float a = to_f32(h.e[j]), d = to_f32(dy.e[j]);
+        float v = rstd * (d * to_f32(w[n])) - a * c;
+        if (p.dh) v += to_f32(o.e[j]);
+        o.e[j] = from_f32<T>(v);
+        dw[n] = fmaf(d * a, rstd, dw[n]);
+        if (!VEC && column(n) < p.cols) dx[column(n)] = o.e[j];
+      }
+      if constexpr (VEC) store16<true>(dx, me + static_cast<int64_t>(i) * threads, p.cols, o, static_cast<T*>(nullptr));
+    }
+  }
+  if constexpr (WARP) {
+    // the block's warps in their order
+    cp_async_wait<0>();
+    float* sums = reinterpret_cast<float*>(ring);
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; ++n) sums[(group * N + n) * 32 + me] = dw[n];
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        float t = dw[n];
+        for (int g = 1; g < kWarpRows; ++g) t += sums[(g * N + n) * 32 + me];
+        if (column(n) < p.cols) p.part[blockIdx.x * p.cols + column(n)] = t;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (column(n) < p.cols) p.part[blockIdx.x * p.cols + column(n)] = dw[n];
+  }
+}
+
+// Rows wider than a block's registers: the row's two sums from a first reading,
 // then dx and the block's dweight row in `part`, accumulated there by the
 // thread that owns the column.
-template <typename T, bool VEC>
+template <typename T>
 __global__ void __launch_bounds__(1024) dbf_rmsnorm_grad_wide_kernel(const NormGradArgs p) {
-  __shared__ float red[2][66];
+  __shared__ float red[2][64];
   pdl_wait();
   pdl_launch_dependents();
   const T* weight = static_cast<const T*>(p.weight);
@@ -221,35 +361,27 @@ __global__ void __launch_bounds__(1024) dbf_rmsnorm_grad_wide_kernel(const NormG
   int flip = 0;
   bool first = true;
   for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x, flip ^= 1, first = false) {
-    const T* hr = static_cast<const T*>(p.h) + r * p.cols;
-    const T* dyr = static_cast<const T*>(p.dy) + r * p.cols;
-    const T* dhr = p.dh ? static_cast<const T*>(p.dh) + r * p.cols : nullptr;
+    const T* h = static_cast<const T*>(p.h) + r * p.cols;
+    const T* dy = static_cast<const T*>(p.dy) + r * p.cols;
+    const T* dh = p.dh ? static_cast<const T*>(p.dh) + r * p.cols : nullptr;
+    T* dx = static_cast<T*>(p.dx) + r * p.cols;
     float hh = 0.f, gh = 0.f;
-    for (int64_t i = 8 * static_cast<int64_t>(threadIdx.x); i < p.cols; i += 8 * blockDim.x) {
-      const Pack8<T> h = load8<VEC>(hr, i, p.cols), dy = load8<VEC>(dyr, i, p.cols), w = load8<VEC>(weight, i, p.cols);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float a = to_f32(h.e[j]);
-        hh = fmaf(a, a, hh);
-        gh = fmaf(to_f32(dy.e[j]) * to_f32(w.e[j]), a, gh);
-      }
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < p.cols; i += blockDim.x) {
+      const float a = to_f32(h[i]);
+      hh = fmaf(a, a, hh);
+      gh = fmaf(to_f32(dy[i]) * to_f32(weight[i]), a, gh);
     }
-    const float2 s = block_sum2(hh, gh, red[flip]);
+    const float2 s = row_sum2<false>(hh, gh, red[flip]);
     const float rstd = 1.f / sqrtf(s.x * inv_cols + p.eps);
     const float c = rstd * rstd * rstd * (s.y * inv_cols);
-    for (int64_t i = 8 * static_cast<int64_t>(threadIdx.x); i < p.cols; i += 8 * blockDim.x) {
-      const Pack8<T> h = load8<VEC>(hr, i, p.cols), dy = load8<VEC>(dyr, i, p.cols), w = load8<VEC>(weight, i, p.cols);
-      Pack8<T> dh, o;
-      if (dhr) dh = load8<VEC>(dhr, i, p.cols);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float a = to_f32(h.e[j]), d = to_f32(dy.e[j]);
-        float v = rstd * (d * to_f32(w.e[j])) - a * c;
-        if (dhr) v += to_f32(dh.e[j]);
-        o.e[j] = from_f32<T>(v);
-        if (i + j < p.cols) part[i + j] = fmaf(d * a, rstd, first ? 0.f : part[i + j]);
-      }
-      store8<VEC>(static_cast<T*>(p.dx) + r * p.cols, i, p.cols, o);
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < p.cols; i += blockDim.x) {
+      const float a = to_f32(h[i]), d = to_f32(dy[i]);
+      float v = rstd * (d * to_f32(weight[i])) - a * c;
+      if (dh) v += to_f32(dh[i]);
+      dx[i] = from_f32<T>(v);
+      part[i] = fmaf(d * a, rstd, first ? 0.f : part[i]);
     }
   }
 }
@@ -274,19 +406,56 @@ __global__ void __launch_bounds__(256) dbf_rmsnorm_grad_sum_kernel(const NormGra
   }
 }
 
-constexpr int64_t kGradRowCols = 8192;  // eight columns for each of 1024 threads
-constexpr int kGradBlocks = 2 * 148;    // rows of `part` at most
+// How the rows are shared out, from the sizes alone (the workspace's size and
+// dweight's order of additions follow from it).
+constexpr int kGradSms = 148;
+struct GradPlan {
+  bool warp;    // a row is one warp's work
+  int nv;       // chunks of sixteen columns per thread; 0: the wide kernel
+  int threads;  // of a block
+  int blocks;   // rows of `part`
+};
+GradPlan grad_plan(int64_t rows, int64_t cols, int elem) {
+  const int64_t chunks = (cols + kChunk - 1) / kChunk;
+  GradPlan g{};
+  g.warp = chunks <= 64;
+  if (g.warp) {
+    g.nv = chunks <= 32 ? 1 : 2;
+    g.threads = 32 * kWarpRows;
+    g.blocks = static_cast<int>(std::min<int64_t>((rows + kWarpRows - 1) / kWarpRows, 2 * kGradSms));
+    return g;
+  }
+  g.nv = chunks <= kGradThreads ? 1 : chunks <= 2 * kGradThreads && elem == 2 ? 2 : 0;
+  g.threads = g.nv ? static_cast<int>(((chunks + g.nv - 1) / g.nv + 31) / 32 * 32) : 1024;
+  const int per_sm = g.nv == 0 ? 2 : g.nv == 2 || g.threads > 256 ? 1 : g.threads > 128 ? 2 : 4;
+  g.blocks = static_cast<int>(std::min<int64_t>(rows, int64_t{kGradSms} * per_sm));
+  return g;
+}
+
+template <typename T, int NV, bool VEC, bool WARP>
+dbf_status launch_grad_kernel(const NormGradArgs& a, const GradPlan& g, const DeviceInfo& dev, cudaStream_t stream) {
+  auto kernel = dbf_rmsnorm_grad_kernel<T, NV, VEC, WARP>;
+  const size_t sums = WARP ? sizeof(float) * kWarpRows * NV * kChunk * 32 : 0;
+  const size_t smem = std::max(sums, VEC ? sizeof(Pack16<T>) * kDepth<T, NV, WARP> * 3 * NV * g.threads : size_t{0});
+  static std::once_flag once[64];  // the attribute once per device
+  static cudaError_t attr_err[64];
+  std::call_once(once[dev.device], [&] {
+    attr_err[dev.device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
+  });
+  if (attr_err[dev.device] != cudaSuccess) return DBF_ERR_CUDA;
+  return launch_pdl(kernel, dim3(g.blocks), dim3(g.threads), smem, stream, a);
+}
 
 template <typename T, bool VEC>
 dbf_status launch_grad(NormGradArgs a, const DeviceInfo& dev, cudaStream_t stream) {
-  a.blocks = static_cast<int>(std::min<int64_t>(a.rows, kGradBlocks));
-  dbf_status st;
-  if (a.cols <= kGradRowCols) {
-    const int threads = static_cast<int>(((a.cols + 7) / 8 + 31) / 32 * 32);
-    st = launch_pdl(dbf_rmsnorm_grad_kernel<T, VEC>, dim3(a.blocks), dim3(threads), 0, stream, a);
-  } else {
-    st = launch_pdl(dbf_rmsnorm_grad_wide_kernel<T, VEC>, dim3(a.blocks), dim3(1024), 0, stream, a);
-  }
+  const GradPlan g = grad_plan(a.rows, a.cols, sizeof(T));
+  a.blocks = g.blocks;
+  const dbf_status st = g.nv == 0              ? launch_pdl(dbf_rmsnorm_grad_wide_kernel<T>, dim3(g.blocks), dim3(g.threads), 0, stream, a)
+                        : g.warp && g.nv == 1 ? launch_grad_kernel<T, 1, VEC, true>(a, g, dev, stream)
+                        : g.warp              ? launch_grad_kernel<T, 2, VEC, true>(a, g, dev, stream)
+                        : g.nv == 1 || sizeof(T) == 4
+                            ? launch_grad_kernel<T, 1, VEC, false>(a, g, dev, stream)
+                            : launch_grad_kernel<T, sizeof(T) == 4 ? 1 : 2, VEC, false>(a, g, dev, stream);
   if (st != DBF_OK) return st;
   return launch_pdl(dbf_rmsnorm_grad_sum_kernel, dim3(static_cast<unsigned>((a.cols + 31) / 32)), dim3(256), 0, stream,
                     a);
@@ -294,8 +463,8 @@ dbf_status launch_grad(NormGradArgs a, const DeviceInfo& dev, cudaStream_t strea
 
 template <typename T>
 dbf_status grad_typed(const NormGradArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
-  const bool vec = a.cols % 8 == 0 && aligned_to(a.dy, 16) && aligned_to(a.h, 16) && aligned_to(a.weight, 16) &&
-                   aligned_to(a.dh, 16) && aligned_to(a.dx, 16);
+  const bool vec = a.cols % kChunk == 0 && aligned_to(a.dy, 16) && aligned_to(a.h, 16) && aligned_to(a.dh, 16) &&
+                   aligned_to(a.dx, 32);
   return vec ? launch_grad<T, true>(a, dev, stream) : launch_grad<T, false>(a, dev, stream);
 }
 
@@ -327,7 +496,6 @@ dbf_status dbf_rmsnorm_forward(const void* x, const void* residual, const void* 
   dbf_status st = check_norm(a, t);
   if (st != DBF_OK) return st;
   if (!aligned_to(y, dtype_size(t))) return DBF_ERR_MISALIGNED;
-  a.pitch = (cols + 7) / 8 * 8;
   DeviceInfo dev;
   st = current_device(&dev);
   if (st != DBF_OK) return st;
@@ -352,7 +520,8 @@ dbf_status dbf_rmsnorm_mx_forward(const void* x, const void* residual, const voi
 
 size_t dbf_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols) {
   if (!norm_shape_ok(rows, cols)) return 0;
-  return static_cast<size_t>(std::min<int64_t>(rows, kGradBlocks)) * static_cast<size_t>(cols) * 4;
+  const int blocks = std::max(grad_plan(rows, cols, 2).blocks, grad_plan(rows, cols, 4).blocks);
+  return static_cast<size_t>(blocks) * static_cast<size_t>(cols) * 4;
 }
 
 dbf_status dbf_rmsnorm_backward(const void* dy, const void* h, const void* weight, const void* dh, dbf_dtype t,
