@@ -8,6 +8,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -136,6 +137,47 @@ template <typename T>
 struct alignas(32) Pack16 {
   T e[kChunk];
 };
+
+// Whole packs at a time: the conversions of two values run at several times the
+// rate of single ones.
+__device__ __forceinline__ void unpack16(const Pack16<float>& p, float (&v)[kChunk]) {
+#pragma unroll
+  for (int j = 0; j < kChunk; ++j) v[j] = p.e[j];
+}
+__device__ __forceinline__ void unpack16(const Pack16<__half>& p, float (&v)[kChunk]) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&p);
+#pragma unroll
+  for (int j = 0; j < kChunk / 2; ++j) {
+    const float2 f = half2_bits_to_float2(w[j]);
+    v[2 * j] = f.x, v[2 * j + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void unpack16(const Pack16<__nv_bfloat16>& p, float (&v)[kChunk]) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(&p);
+#pragma unroll
+  for (int j = 0; j < kChunk / 2; ++j) v[2 * j] = __uint_as_float(w[j] << 16), v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+}
+template <typename T>
+__device__ __forceinline__ Pack16<T> pack16(const float (&v)[kChunk]) {
+  Pack16<T> p;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) p.e[j] = v[j];
+  } else {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&p);
+#pragma unroll
+    for (int j = 0; j < kChunk / 2; ++j) {
+      if constexpr (std::is_same<T, __half>::value) {
+        const __half2 t = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&t);
+      } else {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&t);
+      }
+    }
+  }
+  return p;
+}
 
 // 32-byte accesses (global memory, 32-byte aligned).
 __device__ __forceinline__ void ldg_32(const void* p, uint32_t* r) {

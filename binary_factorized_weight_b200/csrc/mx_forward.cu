@@ -344,12 +344,16 @@ struct PairCfg {
   static constexpr int kScaleOffset = kEpiOffset + kEpiBytes;
   static constexpr int kBarOffset = kScaleOffset + kStages * kScaleBytes;
   static constexpr int kSmemBytes = kBarOffset + 512 + 1024;
+  // scales in tensor memory: a copy may overtake the MMAs issued before it, so a
+  // stage's scales go where no running MMA reads
+  static constexpr int kScaleBufs = 3;
   static constexpr int kScaleCols = 4 * KA * (1 + kQTiles);
-  static constexpr int kScaleBase = 512 - kScaleCols;
+  static constexpr int kScaleBase = 512 - kScaleBufs * kScaleCols;
+  static_assert(kStages > kScaleBufs, "a buffer's last stage must still be told from the next one in its place");
   // the second accumulator starts where it still ends before the scales
   static constexpr int kAcc1 = 2 * NT <= kScaleBase ? NT : (kScaleBase - NT) / 32 * 32;
   static constexpr int kShared = NT - kAcc1;  // columns both accumulators use
-  static_assert(kShared % 32 == 0 && kShared <= 64, "");
+  static_assert(kShared % 32 == 0 && kShared <= 96, "");
 };
 
 struct PairArgs {
@@ -471,16 +475,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait_pair(&acc_shared[b ^ 1], ((n - 1) >> 1) & 1, abort_flag, a.status);
         if (!ok) break;
         const uint32_t d = tmem + b * C::kAcc1;
-        const uint32_t sfa = tmem + C::kScaleBase, sfb = sfa + 4 * KA;
         // where the tile's first weight row lies in its scale tile
         const uint32_t q_col = static_cast<uint32_t>(((t / p_tiles) * NT & 127) >> 5);
         for (int kt = 0; kt < a.stages_k; ++kt, ++it) {
           const int s = static_cast<int>(it % S);
-          if (!mbar_wait_pair(&full[s], (it / S) & 1, abort_flag, a.status)) {
-            ok = false;
-            break;
+          ok = mbar_wait_pair(&full[s], (it / S) & 1, abort_flag, a.status);
+          // the MMAs that read this stage's scale buffer before have completed
+          if (ok && it >= C::kScaleBufs) {
+            const uint32_t old = it - C::kScaleBufs;
+            ok = mbar_wait_pair(&empty[old % S], (old / S) & 1, abort_flag, a.status);
           }
+          if (!ok) break;
           tc_fence_after();
+          const uint32_t sfa = tmem + C::kScaleBase + (it % C::kScaleBufs) * C::kScaleCols, sfb = sfa + 4 * KA;
           const uint32_t sc = smem_u32(s_st + s * C::kScaleBytes);
 #pragma unroll
           for (int k = 0; k < KA; ++k) {

@@ -40,8 +40,7 @@ __global__ void __launch_bounds__(kThreads) dbf_mx_quantize_kernel(const T* __re
     const int64_t c = (it - r * per_row) * 32 + lane;
     const Pack16<T> p = load16<VEC>(src + r * cols, c, cols, stage + (VEC ? 0 : warp * 32 * kChunk));
     float v[kChunk];
-#pragma unroll
-    for (int j = 0; j < kChunk; ++j) v[j] = to_f32(p.e[j]);
+    unpack16(p, v);
     mx_store_row16<FMT>(v, r, c, pitch, codes, scales);
   }
 }
@@ -160,19 +159,22 @@ __global__ void __launch_bounds__(kThreads) dbf_mx_dequantize_kernel(const uint8
     const int64_t c = (it - r * per_row) * 32 + lane;
     Pack16<T> p;
     if (kChunk * c < cols) {
-      float v[2][8];
+      float v[kChunk];
+      float(&lo)[8] = *reinterpret_cast<float(*)[8]>(&v[0]);
+      float(&hi)[8] = *reinterpret_cast<float(*)[8]>(&v[8]);
       if constexpr (FMT == kMx4) {
         const uint2 w = *reinterpret_cast<const uint2*>(codes + (r * pitch >> 1) + 8 * c);
-        mx_decode_e2m1(w.x, v[0]);
-        mx_decode_e2m1(w.y, v[1]);
+        mx_decode_e2m1(w.x, lo);
+        mx_decode_e2m1(w.y, hi);
       } else {
         const uint4 w = *reinterpret_cast<const uint4*>(codes + r * pitch + 16 * c);
-        mx_decode_e4m3(make_uint2(w.x, w.y), v[0]);
-        mx_decode_e4m3(make_uint2(w.z, w.w), v[1]);
+        mx_decode_e4m3(make_uint2(w.x, w.y), lo);
+        mx_decode_e4m3(make_uint2(w.z, w.w), hi);
       }
       const float s = mx_scale(scales[mx_scale_word(r, c >> 3, pitch >> 7) + ((c >> 1) & 3)]);
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) p.e[j] = from_f32<T>(v[j >> 3][j & 7] * s);
+      for (int j = 0; j < kChunk; ++j) v[j] *= s;
+      p = pack16<T>(v);
     }
     store16<VEC>(dst + r * cols, c, cols, p, stage + (VEC ? 0 : warp * 32 * kChunk));
   }

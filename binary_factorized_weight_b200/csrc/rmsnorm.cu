@@ -77,25 +77,29 @@ __global__ void __launch_bounds__(VEC && !WARP ? 1024 : kStagedThreads) dbf_rmsn
     float sum = 0.f;
     auto fetch = [&](int64_t c) {
       Pack16<T> a = load16<VEC>(xr, c, p.cols, stage);
+      float v[kChunk];
+      unpack16(a, v);
       if (rr) {
-        const Pack16<T> b = load16<VEC>(rr, c, p.cols, stage);
+        float u[kChunk];
+        unpack16(load16<VEC>(rr, c, p.cols, stage), u);
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) a.e[j] = from_f32<T>(to_f32(a.e[j]) + to_f32(b.e[j]));
+        for (int j = 0; j < kChunk; ++j) v[j] += u[j];
+        a = pack16<T>(v);
         store16<VEC>(hr, c, p.cols, a, stage);
+        unpack16(a, v);
       }
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) sum = fmaf(to_f32(a.e[j]), to_f32(a.e[j]), sum);
+      for (int j = 0; j < kChunk; ++j) sum = fmaf(v[j], v[j], sum);
       return a;
     };
     auto finish = [&](int64_t c, const Pack16<T>& a, const Pack16<T>& w, float rstd) {
-      float v[kChunk];
+      float v[kChunk], g[kChunk];
+      unpack16(a, v);
+      unpack16(w, g);
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) v[j] = to_f32(a.e[j]) * rstd * to_f32(w.e[j]);
+      for (int j = 0; j < kChunk; ++j) v[j] *= rstd * g[j];
       if constexpr (OUT == kDense) {
-        Pack16<T> o;
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) o.e[j] = from_f32<T>(v[j]);
-        store16<VEC>(static_cast<T*>(p.y) + r * p.cols, c, p.cols, o, stage);
+        store16<VEC>(static_cast<T*>(p.y) + r * p.cols, c, p.cols, pack16<T>(v), stage);
       } else {
         mx_store_row16<OUT>(v, r, c, p.pitch, p.codes, p.scales);
       }
@@ -242,12 +246,25 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kGradThreads, WARP ? 2
                : me + static_cast<int64_t>(n) * threads;
   };
   const float inv_cols = 1.f / static_cast<float>(p.cols);
-  T w[N];
+  Pack16<T> w[NV];
 #pragma unroll
-  for (int n = 0; n < N; ++n)
-    w[n] = column(n) < p.cols ? static_cast<const T*>(p.weight)[column(n)] : from_f32<T>(0.f);
-  // this thread's part of the ring: [stage][operand][NV] packs
-  Pack16<T>* mine = reinterpret_cast<Pack16<T>*>(ring) + static_cast<size_t>(threadIdx.x) * (D * 3 * NV);
+  for (int i = 0; i < NV; ++i) {
+    if constexpr (VEC) {
+      w[i] = load16<true>(static_cast<const T*>(p.weight), me + static_cast<int64_t>(i) * threads, p.cols,
+                          static_cast<T*>(nullptr));
+    } else {
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) {
+        const int64_t c = column(kChunk * i + j);
+        w[i].e[j] = c < p.cols ? static_cast<const T*>(p.weight)[c] : from_f32<T>(0.f);
+      }
+    }
+  }
+  // the ring: [stage][operand][chunk][16-byte part][thread], so that a warp's
+  // accesses are contiguous
+  constexpr int kParts = sizeof(Pack16<T>) / 16;
+  uint4* mine = reinterpret_cast<uint4*>(ring) + threadIdx.x;
+  auto slot = [&](int stage, int o, int i) { return mine + ((stage * 3 + o) * NV + i) * kParts * blockDim.x; };
   auto prefetch = [&](int64_t r, int stage) {
     if constexpr (VEC) {
       if (r < p.rows) {
@@ -256,9 +273,9 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kGradThreads, WARP ? 2
           for (int i = 0; i < NV; ++i) {
             if (column(kChunk * i) < p.cols) {
               const char* from = reinterpret_cast<const char*>(src[o] + r * p.cols + column(kChunk * i));
-              char* to = reinterpret_cast<char*>(mine + (stage * 3 + o) * NV + i);
+              uint4* to = slot(stage, o, i);
 #pragma unroll
-              for (int b = 0; b < static_cast<int>(sizeof(Pack16<T>)); b += 16) cp_async_16(to + b, from + b);
+              for (int b = 0; b < kParts; ++b) cp_async_16(to + b * blockDim.x, from + 16 * b);
             }
           }
         }
@@ -270,7 +287,9 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kGradThreads, WARP ? 2
   auto fetch = [&](int o, int i, int64_t r, int stage) {
     Pack16<T> a;
     if constexpr (VEC) {
-      a = mine[(stage * 3 + o) * NV + i];
+      const uint4* from = slot(stage, o, i);
+#pragma unroll
+      for (int b = 0; b < kParts; ++b) reinterpret_cast<uint4*>(&a)[b] = from[b * blockDim.x];
       if (column(kChunk * i) >= p.cols) {
 #pragma unroll
         for (int j = 0; j < kChunk; ++j) a.e[j] = from_f32<T>(0.f);
@@ -294,12 +313,14 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kGradThreads, WARP ? 2
     float hh = 0.f, gh = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const Pack16<T> h = fetch(0, i, r, stage), dy = fetch(1, i, r, stage);
+      float h[kChunk], dy[kChunk], g[kChunk];
+      unpack16(fetch(0, i, r, stage), h);
+      unpack16(fetch(1, i, r, stage), dy);
+      unpack16(w[i], g);
 #pragma unroll
       for (int j = 0; j < kChunk; ++j) {
-        const float a = to_f32(h.e[j]);
-        hh = fmaf(a, a, hh);
-        gh = fmaf(to_f32(dy.e[j]) * to_f32(w[kChunk * i + j]), a, gh);
+        hh = fmaf(h[j], h[j], hh);
+        gh = fmaf(dy[j] * g[j], h[j], gh);
       }
     }
     const float2 s = row_sum2<WARP>(hh, gh, red[flip]);
@@ -308,20 +329,28 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kGradThreads, WARP ? 2
     T* dx = static_cast<T*>(p.dx) + r * p.cols;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const Pack16<T> h = fetch(0, i, r, stage), dy = fetch(1, i, r, stage);
-      Pack16<T> o;
-      if (p.dh) o = fetch(2, i, r, stage);
+      float h[kChunk], dy[kChunk], g[kChunk];
+      unpack16(fetch(0, i, r, stage), h);
+      unpack16(fetch(1, i, r, stage), dy);
+      unpack16(w[i], g);
 #pragma unroll
       for (int j = 0; j < kChunk; ++j) {
-        const int n = kChunk * i + j;
-        const float a = to_f32(h.e[j]), d = to_f32(dy.e[j]);
-        float v = rstd * (d * to_f32(w[n])) - a * c;
-        if (p.dh) v += to_f32(o.e[j]);
-        o.e[j] = from_f32<T>(v);
-        dw[n] = fmaf(d * a, rstd, dw[n]);
-        if (!VEC && column(n) < p.cols) dx[column(n)] = o.e[j];
+        dw[kChunk * i + j] = fmaf(dy[j] * h[j], rstd, dw[kChunk * i + j]);
+        h[j] = rstd * (dy[j] * g[j]) - h[j] * c;
       }
-      if constexpr (VEC) store16<true>(dx, me + static_cast<int64_t>(i) * threads, p.cols, o, static_cast<T*>(nullptr));
+      if (p.dh) {
+        unpack16(fetch(2, i, r, stage), g);
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) h[j] += g[j];
+      }
+      const Pack16<T> o = pack16<T>(h);
+      if constexpr (VEC) {
+        store16<true>(dx, me + static_cast<int64_t>(i) * threads, p.cols, o, static_cast<T*>(nullptr));
+      } else {
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j)
+          if (column(kChunk * i + j) < p.cols) dx[column(kChunk * i + j)] = o.e[j];
+      }
     }
   }
   if constexpr (WARP) {
@@ -341,9 +370,17 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kGradThreads, WARP ? 2
       }
     }
   } else {
+    float* part = p.part + blockIdx.x * p.cols;
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-      if (column(n) < p.cols) p.part[blockIdx.x * p.cols + column(n)] = dw[n];
+    for (int n = 0; n < N; n += 4) {
+      if (VEC) {
+        if (column(n) < p.cols) *reinterpret_cast<float4*>(part + column(n)) = make_float4(dw[n], dw[n + 1], dw[n + 2], dw[n + 3]);
+      } else {
+#pragma unroll
+        for (int k = n; k < n + 4; ++k)
+          if (column(k) < p.cols) part[column(k)] = dw[k];
+      }
+    }
   }
 }
 
@@ -387,23 +424,29 @@ __global__ void __launch_bounds__(1024) dbf_rmsnorm_grad_wide_kernel(const NormG
 }
 
 // dweight[c] = sum over the blocks' rows of `part`, in their order.  32 columns
-// and 8 runs of rows per block.
-__global__ void __launch_bounds__(256) dbf_rmsnorm_grad_sum_kernel(const NormGradArgs p) {
-  __shared__ float tile[8][33];
+// and 32 runs of rows per block: the loads' latency bounds it, so all of a
+// thread's are under way together.
+constexpr int kSumRuns = 32;
+__global__ void __launch_bounds__(32 * kSumRuns) dbf_rmsnorm_grad_sum_kernel(const NormGradArgs p) {
+  __shared__ float tile[kSumRuns][33];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
   const int64_t c = 32 * static_cast<int64_t>(blockIdx.x) + lane;
   float s = 0.f;
-  if (c < p.cols)
-    for (int b = run; b < p.blocks; b += 8) s += p.part[b * p.cols + c];
+  if (c < p.cols) {
+    const float* part = p.part + c;
+#pragma unroll 10
+    for (int b = run; b < p.blocks; b += kSumRuns) s += part[b * p.cols];
+  }
   tile[run][lane] = s;
   __syncthreads();
-  if (run == 0 && c < p.cols) {
+  // warp `run` adds column `run`'s sums
+  s = tile[lane][run];
 #pragma unroll
-    for (int k = 1; k < 8; ++k) s += tile[k][lane];
-    p.dweight[c] = s;
-  }
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int64_t out = 32 * static_cast<int64_t>(blockIdx.x) + run;
+  if (lane == 0 && out < p.cols) p.dweight[out] = s;
 }
 
 // How the rows are shared out, from the sizes alone (the workspace's size and
@@ -457,14 +500,14 @@ dbf_status launch_grad(NormGradArgs a, const DeviceInfo& dev, cudaStream_t strea
                             ? launch_grad_kernel<T, 1, VEC, false>(a, g, dev, stream)
                             : launch_grad_kernel<T, sizeof(T) == 4 ? 1 : 2, VEC, false>(a, g, dev, stream);
   if (st != DBF_OK) return st;
-  return launch_pdl(dbf_rmsnorm_grad_sum_kernel, dim3(static_cast<unsigned>((a.cols + 31) / 32)), dim3(256), 0, stream,
+  return launch_pdl(dbf_rmsnorm_grad_sum_kernel, dim3(static_cast<unsigned>((a.cols + 31) / 32)), dim3(32 * kSumRuns), 0, stream,
                     a);
 }
 
 template <typename T>
 dbf_status grad_typed(const NormGradArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
   const bool vec = a.cols % kChunk == 0 && aligned_to(a.dy, 16) && aligned_to(a.h, 16) && aligned_to(a.dh, 16) &&
-                   aligned_to(a.dx, 32);
+                   aligned_to(a.weight, 32) && aligned_to(a.dx, 32);
   return vec ? launch_grad<T, true>(a, dev, stream) : launch_grad<T, false>(a, dev, stream);
 }
 
