@@ -179,6 +179,54 @@ __device__ __forceinline__ Pack16<T> pack16(const float (&v)[kChunk]) {
   return p;
 }
 
+// Two fp32 values side by side, for the instructions that work on both.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f2_get(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+constexpr int kPairs = kChunk / 2;
+template <typename T>
+__device__ __forceinline__ void unpack16(const Pack16<T>& p, F2 (&v)[kPairs]) {
+  float t[kChunk];
+  unpack16(p, t);
+#pragma unroll
+  for (int j = 0; j < kPairs; ++j) v[j] = f2(t[2 * j], t[2 * j + 1]);
+}
+template <typename T>
+__device__ __forceinline__ Pack16<T> pack16(const F2 (&v)[kPairs]) {
+  float t[kChunk];
+#pragma unroll
+  for (int j = 0; j < kPairs; ++j) {
+    const float2 a = f2_get(v[j]);
+    t[2 * j] = a.x, t[2 * j + 1] = a.y;
+  }
+  return pack16<T>(t);
+}
+
 // 32-byte accesses (global memory, 32-byte aligned).
 __device__ __forceinline__ void ldg_32(const void* p, uint32_t* r) {
   asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -264,9 +312,13 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
 template <int FMT>
 __device__ __forceinline__ void mx_store_row16(const float (&v)[kChunk], int64_t r, int64_t c, int64_t pitch,
                                                uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-  float m = 0.f;
+  float m0 = 0.f, m1 = 0.f;
 #pragma unroll
-  for (int j = 0; j < kChunk; j += 2) m = max_abs3(m, v[j], v[j + 1]);
+  for (int j = 0; j < kChunk; j += 4) {
+    m0 = max_abs3(m0, v[j], v[j + 1]);
+    m1 = max_abs3(m1, v[j + 2], v[j + 3]);
+  }
+  const float m = max_abs3(m0, m1, 0.f);
   uint32_t amax = __float_as_uint(m) & 0x7FFFFFFFu;
   amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   const uint32_t byte = mx_scale_byte<FMT>(amax);
@@ -279,7 +331,10 @@ __device__ __forceinline__ void mx_store_row16(const float (&v)[kChunk], int64_t
   const float inv = mx_inverse_scale(min(byte, 253u));
   float u[kChunk];
 #pragma unroll
-  for (int j = 0; j < kChunk; ++j) u[j] = v[j] * inv;
+  for (int j = 0; j < kChunk; j += 2) {
+    const float2 t = f2_get(f2_mul(f2(v[j], v[j + 1]), f2(inv, inv)));
+    u[j] = t.x, u[j + 1] = t.y;
+  }
   const float(&lo)[8] = *reinterpret_cast<const float(*)[8]>(&u[0]);
   const float(&hi)[8] = *reinterpret_cast<const float(*)[8]>(&u[8]);
   if constexpr (FMT == kMx4) {

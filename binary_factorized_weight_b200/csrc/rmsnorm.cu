@@ -74,52 +74,70 @@ __global__ void __launch_bounds__(VEC && !WARP ? 1024 : kStagedThreads) dbf_rmsn
     const T* xr = x + r * p.cols;
     const T* rr = res ? res + r * p.cols : nullptr;
     T* hr = res ? static_cast<T*>(p.h) + r * p.cols : nullptr;
-    float sum = 0.f;
-    auto fetch = [&](int64_t c) {
-      Pack16<T> a = load16<VEC>(xr, c, p.cols, stage);
-      float v[kChunk];
+    F2 sums = f2(0.f, 0.f);
+    auto add = [&](int64_t c, Pack16<T> a, const Pack16<T>& b) {
+      F2 v[kPairs];
       unpack16(a, v);
       if (rr) {
-        float u[kChunk];
-        unpack16(load16<VEC>(rr, c, p.cols, stage), u);
+        F2 u[kPairs];
+        unpack16(b, u);
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) v[j] += u[j];
+        for (int j = 0; j < kPairs; ++j) v[j] = f2_add(v[j], u[j]);
         a = pack16<T>(v);
         store16<VEC>(hr, c, p.cols, a, stage);
         unpack16(a, v);
       }
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) sum = fmaf(v[j], v[j], sum);
+      for (int j = 0; j < kPairs; ++j) sums = f2_fma(v[j], v[j], sums);
       return a;
     };
+    auto rstd_of = [&]() {
+      const float2 t = f2_get(sums);
+      return 1.f / sqrtf(row_sum<WARP>(t.x + t.y, red[flip]) * inv_cols + p.eps);
+    };
     auto finish = [&](int64_t c, const Pack16<T>& a, const Pack16<T>& w, float rstd) {
-      float v[kChunk], g[kChunk];
+      F2 v[kPairs], g[kPairs];
       unpack16(a, v);
       unpack16(w, g);
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) v[j] *= rstd * g[j];
+      for (int j = 0; j < kPairs; ++j) v[j] = f2_mul(f2_mul(v[j], f2(rstd, rstd)), g[j]);
       if constexpr (OUT == kDense) {
         store16<VEC>(static_cast<T*>(p.y) + r * p.cols, c, p.cols, pack16<T>(v), stage);
       } else {
-        mx_store_row16<OUT>(v, r, c, p.pitch, p.codes, p.scales);
+        float t[kChunk];
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          const float2 e = f2_get(v[j]);
+          t[2 * j] = e.x, t[2 * j + 1] = e.y;
+        }
+        mx_store_row16<OUT>(t, r, c, p.pitch, p.codes, p.scales);
       }
     };
     if constexpr (NV > 0) {
-      Pack16<T> a[NV], w[NV];
+      // all loads before the first use
+      Pack16<T> a[NV], b[NV], w[NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int64_t c = me + i * threads;
-        a[i] = fetch(c);
-        w[i] = load16<VEC>(weight, c, p.cols, stage);
+        a[i] = load16<VEC>(xr, c, p.cols, stage);
+        if (rr) b[i] = load16<VEC>(rr, c, p.cols, stage);
       }
-      const float rstd = 1.f / sqrtf(row_sum<WARP>(sum, red[flip]) * inv_cols + p.eps);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) w[i] = load16<VEC>(weight, me + i * threads, p.cols, stage);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) a[i] = add(me + i * threads, a[i], b[i]);
+      const float rstd = rstd_of();
 #pragma unroll
       for (int i = 0; i < NV; ++i) finish(me + i * threads, a[i], w[i], rstd);
     } else {
       // a whole number of rounds for every thread: staging and the MX store are a warp's work
       const int64_t rounds = ((p.pitch + kChunk - 1) / kChunk + threads - 1) / threads;
-      for (int64_t i = 0; i < rounds; ++i) fetch(me + i * threads);
-      const float rstd = 1.f / sqrtf(row_sum<WARP>(sum, red[flip]) * inv_cols + p.eps);
+      for (int64_t i = 0; i < rounds; ++i) {
+        const int64_t c = me + i * threads;
+        const Pack16<T> a = load16<VEC>(xr, c, p.cols, stage);
+        add(c, a, rr ? load16<VEC>(rr, c, p.cols, stage) : a);
+      }
+      const float rstd = rstd_of();
       const T* again = rr ? hr : xr;
       for (int64_t i = 0; i < rounds; ++i) {
         const int64_t c = me + i * threads;
@@ -181,28 +199,30 @@ struct NormGradArgs {
   float eps;
 };
 
-// Sums of two values per thread over the row's threads; red: 64 floats.
-template <bool WARP>
-__device__ __forceinline__ float2 row_sum2(float a, float b, float* red) {
+// Sums of M values per thread over the row's threads; red: 32 M floats.
+template <bool WARP, int M>
+__device__ __forceinline__ void row_sums(float (&v)[M], float* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b += __shfl_xor_sync(0xffffffffu, b, o);
+#pragma unroll
+    for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
   }
-  if (WARP) return make_float2(a, b);
+  if (WARP) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  if (lane == 0) {
-    red[warp] = a;
-    red[32 + warp] = b;
+  if (lane < M) {
+    float mine = v[0];
+#pragma unroll
+    for (int m = 1; m < M; ++m) mine = lane == m ? v[m] : mine;
+    red[warp * M + lane] = mine;
   }
   __syncthreads();
-  float s = lane < warps ? red[lane] : 0.f, t = lane < warps ? red[32 + lane] : 0.f;
+#pragma unroll
+  for (int m = 0; m < M; ++m) v[m] = lane < warps ? red[lane * M + m] : 0.f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    s += __shfl_xor_sync(0xffffffffu, s, o);
-    t += __shfl_xor_sync(0xffffffffu, t, o);
+#pragma unroll
+    for (int m = 0; m < M; ++m) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
   }
-  return make_float2(s, t);
 }
 
 __device__ __forceinline__ void cp_async_16(void* smem_dst, const void* src) {
@@ -223,21 +243,24 @@ __device__ __forceinline__ void cp_async_wait() {
 // sums and once for the gradients.  Else it owns every threads-th column and
 // reads it where it is, the second time from L1.
 constexpr int kGradThreads = 512;
-// rows of the ring: as many as a block of kGradThreads has room for
+// Rows that are reduced together (one barrier and one latency for both), and
+// stages of that many rows in the ring: what a block of kGradThreads has room for.
+template <typename T, int NV>
+constexpr int kGradRows = NV * sizeof(T) == 2 ? 2 : 1;
 template <typename T, int NV, bool WARP>
-constexpr int kDepth = WARP || NV * sizeof(T) == 2 ? 3 : 2;
+constexpr int kDepth = WARP && NV * sizeof(T) != 2 ? 3 : 2;
 template <typename T, int NV, bool VEC, bool WARP>
 __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kGradThreads, WARP ? 2 : 1)
     dbf_rmsnorm_grad_kernel(const NormGradArgs p) {
-  constexpr int N = NV * kChunk, D = kDepth<T, NV, WARP>;
-  __shared__ float red[2][64];
+  constexpr int N = NV * kChunk, D = kDepth<T, NV, WARP>, R = kGradRows<T, NV>;
+  __shared__ float red[2][32 * 2 * R];
   extern __shared__ uint8_t ring[];
   pdl_wait();
   pdl_launch_dependents();
   const int me = WARP ? threadIdx.x & 31 : threadIdx.x, threads = WARP ? 32 : blockDim.x;
   const int group = WARP ? threadIdx.x >> 5 : 0;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * (WARP ? kWarpRows : 1) + group;
-  const int64_t row_step = static_cast<int64_t>(gridDim.x) * (WARP ? kWarpRows : 1);
+  const int64_t row_step = static_cast<int64_t>(gridDim.x) * (WARP ? kWarpRows : 1);  // R of them an iteration
   const T* src[3] = {static_cast<const T*>(p.h), static_cast<const T*>(p.dy), static_cast<const T*>(p.dh)};
   const int operands = p.dh ? 3 : 2;
   // column of this thread's element n
@@ -260,20 +283,26 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kGradThreads, WARP ? 2
       }
     }
   }
-  // the ring: [stage][operand][chunk][16-byte part][thread], so that a warp's
-  // accesses are contiguous
+  // the ring: [stage][row][operand][chunk][16-byte part][thread], so that a
+  // warp's accesses are contiguous
   constexpr int kParts = sizeof(Pack16<T>) / 16;
   uint4* mine = reinterpret_cast<uint4*>(ring) + threadIdx.x;
-  auto slot = [&](int stage, int o, int i) { return mine + ((stage * 3 + o) * NV + i) * kParts * blockDim.x; };
+  auto slot = [&](int stage, int q, int o, int i) {
+    return mine + (((stage * R + q) * 3 + o) * NV + i) * kParts * blockDim.x;
+  };
   auto prefetch = [&](int64_t r, int stage) {
     if constexpr (VEC) {
-      if (r < p.rows) {
-        for (int o = 0; o < operands; ++o) {
+#pragma unroll
+      for (int q = 0; q < R; ++q, r += row_step) {
+        if (r >= p.rows) break;
+#pragma unroll
+        for (int o = 0; o < 3; ++o) {
+          if (o >= operands) break;
 #pragma unroll
           for (int i = 0; i < NV; ++i) {
             if (column(kChunk * i) < p.cols) {
               const char* from = reinterpret_cast<const char*>(src[o] + r * p.cols + column(kChunk * i));
-              uint4* to = slot(stage, o, i);
+              uint4* to = slot(stage, q, o, i);
 #pragma unroll
               for (int b = 0; b < kParts; ++b) cp_async_16(to + b * blockDim.x, from + 16 * b);
             }
@@ -283,17 +312,13 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kGradThreads, WARP ? 2
       cp_async_commit();
     }
   };
-  // sixteen of this thread's elements of an operand's row
-  auto fetch = [&](int o, int i, int64_t r, int stage) {
+  // sixteen of this thread's elements of an operand's row (zero behind the last column)
+  auto fetch = [&](int o, int i, int64_t r, int q, int stage, F2 (&v)[kPairs]) {
     Pack16<T> a;
     if constexpr (VEC) {
-      const uint4* from = slot(stage, o, i);
+      const uint4* from = slot(stage, q, o, i);
 #pragma unroll
       for (int b = 0; b < kParts; ++b) reinterpret_cast<uint4*>(&a)[b] = from[b * blockDim.x];
-      if (column(kChunk * i) >= p.cols) {
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) a.e[j] = from_f32<T>(0.f);
-      }
     } else {
 #pragma unroll
       for (int j = 0; j < kChunk; ++j) {
@@ -301,57 +326,90 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kGradThreads, WARP ? 2
         a.e[j] = c < p.cols ? src[o][r * p.cols + c] : from_f32<T>(0.f);
       }
     }
-    return a;
+    unpack16(a, v);
   };
-  float dw[N] = {};
+  if constexpr (VEC) {  // the slots of columns behind the last stay zero
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (column(kChunk * i) < p.cols) continue;
+      for (int k = 0; k < D * R * 3; ++k) {
+#pragma unroll
+        for (int b = 0; b < kParts; ++b) slot(0, 0, k, i)[b * blockDim.x] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  }
+  F2 dw[N / 2];
+#pragma unroll
+  for (int n = 0; n < N / 2; ++n) dw[n] = f2(0.f, 0.f);
   int flip = 0, stage = 0;
 #pragma unroll
-  for (int d = 0; d < D - 1; ++d) prefetch(row0 + d * row_step, d);
-  for (int64_t r = row0; r < p.rows; r += row_step, flip ^= 1, stage = stage + 1 == D ? 0 : stage + 1) {
-    prefetch(r + (D - 1) * row_step, stage == 0 ? D - 1 : stage - 1);
+  for (int d = 0; d < D - 1; ++d) prefetch(row0 + d * R * row_step, d);
+  for (int64_t r0 = row0; r0 < p.rows; r0 += R * row_step, flip ^= 1, stage = stage + 1 == D ? 0 : stage + 1) {
+    prefetch(r0 + (D - 1) * R * row_step, stage == 0 ? D - 1 : stage - 1);
     cp_async_wait<D - 1>();
-    float hh = 0.f, gh = 0.f;
+    float s[2 * R] = {};  // per row: sum of h h, sum of g h
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float h[kChunk], dy[kChunk], g[kChunk];
-      unpack16(fetch(0, i, r, stage), h);
-      unpack16(fetch(1, i, r, stage), dy);
-      unpack16(w[i], g);
+    for (int q = 0; q < R; ++q) {
+      if (r0 + q * row_step >= p.rows) break;
+      F2 hh = f2(0.f, 0.f), gh = hh;
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) {
-        hh = fmaf(h[j], h[j], hh);
-        gh = fmaf(dy[j] * g[j], h[j], gh);
+      for (int i = 0; i < NV; ++i) {
+        F2 h[kPairs], dy[kPairs], g[kPairs];
+        fetch(0, i, r0 + q * row_step, q, stage, h);
+        fetch(1, i, r0 + q * row_step, q, stage, dy);
+        unpack16(w[i], g);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          hh = f2_fma(h[j], h[j], hh);
+          gh = f2_fma(f2_mul(dy[j], g[j]), h[j], gh);
+        }
+      }
+      const float2 a = f2_get(hh), b = f2_get(gh);
+      s[2 * q] = a.x + a.y;
+      s[2 * q + 1] = b.x + b.y;
+    }
+    row_sums<WARP, 2 * R>(s, red[flip]);
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const int64_t r = r0 + q * row_step;
+      if (r >= p.rows) break;
+      const float rstd = 1.f / sqrtf(s[2 * q] * inv_cols + p.eps);
+      const float c = -(rstd * rstd * rstd * (s[2 * q + 1] * inv_cols));
+      const F2 rstd2 = f2(rstd, rstd), c2 = f2(c, c);
+      T* dx = static_cast<T*>(p.dx) + r * p.cols;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        F2 h[kPairs], dy[kPairs], g[kPairs];
+        fetch(0, i, r, q, stage, h);
+        fetch(1, i, r, q, stage, dy);
+        unpack16(w[i], g);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          const F2 t = f2_mul(dy[j], rstd2);
+          dw[kPairs * i + j] = f2_fma(t, h[j], dw[kPairs * i + j]);
+          h[j] = f2_fma(h[j], c2, f2_mul(t, g[j]));
+        }
+        if (p.dh) {
+          fetch(2, i, r, q, stage, g);
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) h[j] = f2_add(h[j], g[j]);
+        }
+        const Pack16<T> o = pack16<T>(h);
+        if constexpr (VEC) {
+          store16<true>(dx, me + static_cast<int64_t>(i) * threads, p.cols, o, static_cast<T*>(nullptr));
+        } else {
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j)
+            if (column(kChunk * i + j) < p.cols) dx[column(kChunk * i + j)] = o.e[j];
+        }
       }
     }
-    const float2 s = row_sum2<WARP>(hh, gh, red[flip]);
-    const float rstd = 1.f / sqrtf(s.x * inv_cols + p.eps);
-    const float c = rstd * rstd * rstd * (s.y * inv_cols);
-    T* dx = static_cast<T*>(p.dx) + r * p.cols;
+  }
+  float dws[N];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float h[kChunk], dy[kChunk], g[kChunk];
-      unpack16(fetch(0, i, r, stage), h);
-      unpack16(fetch(1, i, r, stage), dy);
-      unpack16(w[i], g);
-#pragma unroll
-      for (int j = 0; j < kChunk; ++j) {
-        dw[kChunk * i + j] = fmaf(dy[j] * h[j], rstd, dw[kChunk * i + j]);
-        h[j] = rstd * (dy[j] * g[j]) - h[j] * c;
-      }
-      if (p.dh) {
-        unpack16(fetch(2, i, r, stage), g);
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) h[j] += g[j];
-      }
-      const Pack16<T> o = pack16<T>(h);
-      if constexpr (VEC) {
-        store16<true>(dx, me + static_cast<int64_t>(i) * threads, p.cols, o, static_cast<T*>(nullptr));
-      } else {
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j)
-          if (column(kChunk * i + j) < p.cols) dx[column(kChunk * i + j)] = o.e[j];
-      }
-    }
+  for (int n = 0; n < N / 2; ++n) {
+    const float2 t = f2_get(dw[n]);
+    dws[2 * n] = t.x, dws[2 * n + 1] = t.y;
   }
   if constexpr (WARP) {
     // the block's warps in their order
@@ -359,12 +417,12 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kGradThreads, WARP ? 2
     float* sums = reinterpret_cast<float*>(ring);
     __syncthreads();
 #pragma unroll
-    for (int n = 0; n < N; ++n) sums[(group * N + n) * 32 + me] = dw[n];
+    for (int n = 0; n < N; ++n) sums[(group * N + n) * 32 + me] = dws[n];
     __syncthreads();
     if (group == 0) {
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        float t = dw[n];
+        float t = dws[n];
         for (int g = 1; g < kWarpRows; ++g) t += sums[(g * N + n) * 32 + me];
         if (column(n) < p.cols) p.part[blockIdx.x * p.cols + column(n)] = t;
       }
@@ -374,11 +432,11 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kGradThreads, WARP ? 2
 #pragma unroll
     for (int n = 0; n < N; n += 4) {
       if (VEC) {
-        if (column(n) < p.cols) *reinterpret_cast<float4*>(part + column(n)) = make_float4(dw[n], dw[n + 1], dw[n + 2], dw[n + 3]);
+        if (column(n) < p.cols) *reinterpret_cast<float4*>(part + column(n)) = make_float4(dws[n], dws[n + 1], dws[n + 2], dws[n + 3]);
       } else {
 #pragma unroll
         for (int k = n; k < n + 4; ++k)
-          if (column(k) < p.cols) part[column(k)] = dw[k];
+          if (column(k) < p.cols) part[column(k)] = dws[k];
       }
     }
   }
@@ -409,9 +467,10 @@ __global__ void __launch_bounds__(1024) dbf_rmsnorm_grad_wide_kernel(const NormG
       hh = fmaf(a, a, hh);
       gh = fmaf(to_f32(dy[i]) * to_f32(weight[i]), a, gh);
     }
-    const float2 s = row_sum2<false>(hh, gh, red[flip]);
-    const float rstd = 1.f / sqrtf(s.x * inv_cols + p.eps);
-    const float c = rstd * rstd * rstd * (s.y * inv_cols);
+    float s[2] = {hh, gh};
+    row_sums<false, 2>(s, red[flip]);
+    const float rstd = 1.f / sqrtf(s[0] * inv_cols + p.eps);
+    const float c = rstd * rstd * rstd * (s[1] * inv_cols);
 #pragma unroll 4
     for (int64_t i = threadIdx.x; i < p.cols; i += blockDim.x) {
       const float a = to_f32(h[i]), d = to_f32(dy[i]);
@@ -479,7 +538,7 @@ template <typename T, int NV, bool VEC, bool WARP>
 dbf_status launch_grad_kernel(const NormGradArgs& a, const GradPlan& g, const DeviceInfo& dev, cudaStream_t stream) {
   auto kernel = dbf_rmsnorm_grad_kernel<T, NV, VEC, WARP>;
   const size_t sums = WARP ? sizeof(float) * kWarpRows * NV * kChunk * 32 : 0;
-  const size_t smem = std::max(sums, VEC ? sizeof(Pack16<T>) * kDepth<T, NV, WARP> * 3 * NV * g.threads : size_t{0});
+  const size_t smem = std::max(sums, VEC ? sizeof(Pack16<T>) * kDepth<T, NV, WARP> * kGradRows<T, NV> * 3 * NV * g.threads : size_t{0});
   static std::once_flag once[64];  // the attribute once per device
   static cudaError_t attr_err[64];
   std::call_once(once[dev.device], [&] {
@@ -500,6 +559,13 @@ dbf_status launch_grad(NormGradArgs a, const DeviceInfo& dev, cudaStream_t strea
                             ? launch_grad_kernel<T, 1, VEC, false>(a, g, dev, stream)
                             : launch_grad_kernel<T, sizeof(T) == 4 ? 1 : 2, VEC, false>(a, g, dev, stream);
   if (st != DBF_OK) return st;
+  // the same division of shared memory and L1 as the kernel before: a change
+  // between two kernels keeps the second from starting beside the first
+  static std::once_flag once[64];
+  std::call_once(once[dev.device], [&] {
+    (void)cudaFuncSetAttribute(dbf_rmsnorm_grad_sum_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
+  });
   return launch_pdl(dbf_rmsnorm_grad_sum_kernel, dim3(static_cast<unsigned>((a.cols + 31) / 32)), dim3(32 * kSumRuns), 0, stream,
                     a);
 }
