@@ -8,7 +8,6 @@
 // The sums are fp32.  Every operand is read once where a row fits the block's
 // registers, so DRAM bounds all of it; few rows are bound by latency.
 #include <algorithm>
-#include <mutex>
 
 #include "dbf_internal.h"
 #include "mx_device.cuh"
@@ -225,185 +224,115 @@ __device__ __forceinline__ void row_sums(float (&v)[M], float* red) {
   }
 }
 
-__device__ __forceinline__ void cp_async_16(void* smem_dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem_dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // A row is the work of one warp (WARP, eight rows to a block) or of a block;
 // NV * 16 columns per thread, whose sums of dweight over the rows stay in
 // registers and go to the block's row of `part`.
-// VEC: a thread copies its own columns of the rows to come into shared memory
-// (cp.async), so loads are under way all the time and no thread waits for
-// another's; it owns sixteen neighbouring columns and reads them once for the
-// sums and once for the gradients.  Else it owns every threads-th column and
-// reads it where it is, the second time from L1.
+// VEC: a thread owns sixteen neighbouring columns (32-byte accesses); else every
+// threads-th column.  PRE: the next row is loaded while this one is reduced (16-
+// bit elements, sixteen to a thread: more does not fit the registers).
 constexpr int kGradThreads = 512;
-// Rows that are reduced together (one barrier and one latency for both), and
-// stages of that many rows in the ring: what a block of kGradThreads has room for.
-template <typename T, int NV>
-constexpr int kGradRows = NV * sizeof(T) == 2 ? 2 : 1;
-template <typename T, int NV, bool WARP>
-constexpr int kDepth = WARP && NV * sizeof(T) != 2 ? 3 : 2;
 template <typename T, int NV, bool VEC, bool WARP>
 __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kGradThreads, WARP ? 2 : 1)
     dbf_rmsnorm_grad_kernel(const NormGradArgs p) {
-  constexpr int N = NV * kChunk, D = kDepth<T, NV, WARP>, R = kGradRows<T, NV>;
-  __shared__ float red[2][32 * 2 * R];
-  extern __shared__ uint8_t ring[];
+  constexpr int N = NV * kChunk;
+  constexpr bool PRE = NV * sizeof(T) == 2;
+  __shared__ float red[2][64];
+  __shared__ float sums[WARP ? kWarpRows * N * 32 : 1];
   pdl_wait();
   pdl_launch_dependents();
   const int me = WARP ? threadIdx.x & 31 : threadIdx.x, threads = WARP ? 32 : blockDim.x;
   const int group = WARP ? threadIdx.x >> 5 : 0;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * (WARP ? kWarpRows : 1) + group;
-  const int64_t row_step = static_cast<int64_t>(gridDim.x) * (WARP ? kWarpRows : 1);  // R of them an iteration
-  const T* src[3] = {static_cast<const T*>(p.h), static_cast<const T*>(p.dy), static_cast<const T*>(p.dh)};
-  const int operands = p.dh ? 3 : 2;
+  const int64_t row_step = static_cast<int64_t>(gridDim.x) * (WARP ? kWarpRows : 1);
   // column of this thread's element n
   auto column = [&](int n) -> int64_t {
     return VEC ? kChunk * (me + static_cast<int64_t>(n / kChunk) * threads) + n % kChunk
                : me + static_cast<int64_t>(n) * threads;
   };
-  const float inv_cols = 1.f / static_cast<float>(p.cols);
-  Pack16<T> w[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if constexpr (VEC) {
-      w[i] = load16<true>(static_cast<const T*>(p.weight), me + static_cast<int64_t>(i) * threads, p.cols,
-                          static_cast<T*>(nullptr));
-    } else {
-#pragma unroll
-      for (int j = 0; j < kChunk; ++j) {
-        const int64_t c = column(kChunk * i + j);
-        w[i].e[j] = c < p.cols ? static_cast<const T*>(p.weight)[c] : from_f32<T>(0.f);
-      }
-    }
-  }
-  // the ring: [stage][row][operand][chunk][16-byte part][thread], so that a
-  // warp's accesses are contiguous
-  constexpr int kParts = sizeof(Pack16<T>) / 16;
-  uint4* mine = reinterpret_cast<uint4*>(ring) + threadIdx.x;
-  auto slot = [&](int stage, int q, int o, int i) {
-    return mine + (((stage * R + q) * 3 + o) * NV + i) * kParts * blockDim.x;
-  };
-  auto prefetch = [&](int64_t r, int stage) {
-    if constexpr (VEC) {
-#pragma unroll
-      for (int q = 0; q < R; ++q, r += row_step) {
-        if (r >= p.rows) break;
-#pragma unroll
-        for (int o = 0; o < 3; ++o) {
-          if (o >= operands) break;
-#pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            if (column(kChunk * i) < p.cols) {
-              const char* from = reinterpret_cast<const char*>(src[o] + r * p.cols + column(kChunk * i));
-              uint4* to = slot(stage, q, o, i);
-#pragma unroll
-              for (int b = 0; b < kParts; ++b) cp_async_16(to + b * blockDim.x, from + 16 * b);
-            }
-          }
-        }
-      }
-      cp_async_commit();
-    }
-  };
-  // sixteen of this thread's elements of an operand's row (zero behind the last column)
-  auto fetch = [&](int o, int i, int64_t r, int q, int stage, F2 (&v)[kPairs]) {
-    Pack16<T> a;
-    if constexpr (VEC) {
-      const uint4* from = slot(stage, q, o, i);
-#pragma unroll
-      for (int b = 0; b < kParts; ++b) reinterpret_cast<uint4*>(&a)[b] = from[b * blockDim.x];
-    } else {
-#pragma unroll
-      for (int j = 0; j < kChunk; ++j) {
-        const int64_t c = column(kChunk * i + j);
-        a.e[j] = c < p.cols ? src[o][r * p.cols + c] : from_f32<T>(0.f);
-      }
-    }
-    unpack16(a, v);
-  };
-  if constexpr (VEC) {  // the slots of columns behind the last stay zero
+  // this thread's elements of a row (zero behind the last column)
+  auto load = [&](const void* base, int64_t r, Pack16<T> (&a)[NV]) {
+    const T* row = static_cast<const T*>(base) + r * p.cols;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (column(kChunk * i) < p.cols) continue;
-      for (int k = 0; k < D * R * 3; ++k) {
+      if constexpr (VEC) {
+        a[i] = load16<true>(row, me + static_cast<int64_t>(i) * threads, p.cols, static_cast<T*>(nullptr));
+      } else {
 #pragma unroll
-        for (int b = 0; b < kParts; ++b) slot(0, 0, k, i)[b * blockDim.x] = make_uint4(0u, 0u, 0u, 0u);
+        for (int j = 0; j < kChunk; ++j) {
+          const int64_t c = column(kChunk * i + j);
+          a[i].e[j] = c < p.cols ? row[c] : from_f32<T>(0.f);
+        }
       }
     }
-  }
+  };
+  struct Row {
+    Pack16<T> h[NV], dy[NV], dh[NV];
+  };
+  auto load_row = [&](int64_t r, Row& a) {
+    load(p.h, r, a.h);
+    load(p.dy, r, a.dy);
+    if (p.dh) load(p.dh, r, a.dh);
+  };
+  const float inv_cols = 1.f / static_cast<float>(p.cols);
+  Row a;
+  if (row0 < p.rows) load_row(row0, a);
+  Pack16<T> w[NV];
+  load(p.weight, 0, w);
   F2 dw[N / 2];
 #pragma unroll
   for (int n = 0; n < N / 2; ++n) dw[n] = f2(0.f, 0.f);
-  int flip = 0, stage = 0;
+  int flip = 0;
+  for (int64_t r = row0; r < p.rows; r += row_step, flip ^= 1) {
+    Row next;
+    if (PRE && r + row_step < p.rows) load_row(r + row_step, next);
+    F2 hh = f2(0.f, 0.f), gh = hh;
 #pragma unroll
-  for (int d = 0; d < D - 1; ++d) prefetch(row0 + d * R * row_step, d);
-  for (int64_t r0 = row0; r0 < p.rows; r0 += R * row_step, flip ^= 1, stage = stage + 1 == D ? 0 : stage + 1) {
-    prefetch(r0 + (D - 1) * R * row_step, stage == 0 ? D - 1 : stage - 1);
-    cp_async_wait<D - 1>();
-    float s[2 * R] = {};  // per row: sum of h h, sum of g h
+    for (int i = 0; i < NV; ++i) {
+      F2 h[kPairs], dy[kPairs], g[kPairs];
+      unpack16(a.h[i], h);
+      unpack16(a.dy[i], dy);
+      unpack16(w[i], g);
 #pragma unroll
-    for (int q = 0; q < R; ++q) {
-      if (r0 + q * row_step >= p.rows) break;
-      F2 hh = f2(0.f, 0.f), gh = hh;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        F2 h[kPairs], dy[kPairs], g[kPairs];
-        fetch(0, i, r0 + q * row_step, q, stage, h);
-        fetch(1, i, r0 + q * row_step, q, stage, dy);
-        unpack16(w[i], g);
-#pragma unroll
-        for (int j = 0; j < kPairs; ++j) {
-          hh = f2_fma(h[j], h[j], hh);
-          gh = f2_fma(f2_mul(dy[j], g[j]), h[j], gh);
-        }
-      }
-      const float2 a = f2_get(hh), b = f2_get(gh);
-      s[2 * q] = a.x + a.y;
-      s[2 * q + 1] = b.x + b.y;
-    }
-    row_sums<WARP, 2 * R>(s, red[flip]);
-#pragma unroll
-    for (int q = 0; q < R; ++q) {
-      const int64_t r = r0 + q * row_step;
-      if (r >= p.rows) break;
-      const float rstd = 1.f / sqrtf(s[2 * q] * inv_cols + p.eps);
-      const float c = -(rstd * rstd * rstd * (s[2 * q + 1] * inv_cols));
-      const F2 rstd2 = f2(rstd, rstd), c2 = f2(c, c);
-      T* dx = static_cast<T*>(p.dx) + r * p.cols;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        F2 h[kPairs], dy[kPairs], g[kPairs];
-        fetch(0, i, r, q, stage, h);
-        fetch(1, i, r, q, stage, dy);
-        unpack16(w[i], g);
-#pragma unroll
-        for (int j = 0; j < kPairs; ++j) {
-          const F2 t = f2_mul(dy[j], rstd2);
-          dw[kPairs * i + j] = f2_fma(t, h[j], dw[kPairs * i + j]);
-          h[j] = f2_fma(h[j], c2, f2_mul(t, g[j]));
-        }
-        if (p.dh) {
-          fetch(2, i, r, q, stage, g);
-#pragma unroll
-          for (int j = 0; j < kPairs; ++j) h[j] = f2_add(h[j], g[j]);
-        }
-        const Pack16<T> o = pack16<T>(h);
-        if constexpr (VEC) {
-          store16<true>(dx, me + static_cast<int64_t>(i) * threads, p.cols, o, static_cast<T*>(nullptr));
-        } else {
-#pragma unroll
-          for (int j = 0; j < kChunk; ++j)
-            if (column(kChunk * i + j) < p.cols) dx[column(kChunk * i + j)] = o.e[j];
-        }
+      for (int j = 0; j < kPairs; ++j) {
+        hh = f2_fma(h[j], h[j], hh);
+        gh = f2_fma(f2_mul(dy[j], g[j]), h[j], gh);
       }
     }
+    const float2 th = f2_get(hh), tg = f2_get(gh);
+    float s[2] = {th.x + th.y, tg.x + tg.y};
+    row_sums<WARP, 2>(s, red[flip]);
+    const float rstd = 1.f / sqrtf(s[0] * inv_cols + p.eps);
+    const float c = -(rstd * rstd * rstd * (s[1] * inv_cols));
+    const F2 rstd2 = f2(rstd, rstd), c2 = f2(c, c);
+    T* dx = static_cast<T*>(p.dx) + r * p.cols;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      F2 h[kPairs], dy[kPairs], g[kPairs];
+      unpack16(a.h[i], h);
+      unpack16(a.dy[i], dy);
+      unpack16(w[i], g);
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        const F2 t = f2_mul(dy[j], rstd2);
+        dw[kPairs * i + j] = f2_fma(t, h[j], dw[kPairs * i + j]);
+        h[j] = f2_fma(h[j], c2, f2_mul(t, g[j]));
+      }
+      if (p.dh) {
+        unpack16(a.dh[i], g);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) h[j] = f2_add(h[j], g[j]);
+      }
+      const Pack16<T> o = pack16<T>(h);
+      if constexpr (VEC) {
+        store16<true>(dx, me + static_cast<int64_t>(i) * threads, p.cols, o, static_cast<T*>(nullptr));
+      } else {
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j)
+          if (column(kChunk * i + j) < p.cols) dx[column(kChunk * i + j)] = o.e[j];
+      }
+    }
+    if (PRE) a = next;
+    else if (r + row_step < p.rows) load_row(r + row_step, a);
   }
   float dws[N];
 #pragma unroll
@@ -411,24 +340,19 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kGradThreads, WARP ? 2
     const float2 t = f2_get(dw[n]);
     dws[2 * n] = t.x, dws[2 * n + 1] = t.y;
   }
+  float* part = p.part + blockIdx.x * p.cols;
   if constexpr (WARP) {
     // the block's warps in their order
-    cp_async_wait<0>();
-    float* sums = reinterpret_cast<float*>(ring);
-    __syncthreads();
 #pragma unroll
     for (int n = 0; n < N; ++n) sums[(group * N + n) * 32 + me] = dws[n];
     __syncthreads();
-    if (group == 0) {
+    for (int n = group; n < N; n += kWarpRows) {
+      float t = 0.f;
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        float t = dws[n];
-        for (int g = 1; g < kWarpRows; ++g) t += sums[(g * N + n) * 32 + me];
-        if (column(n) < p.cols) p.part[blockIdx.x * p.cols + column(n)] = t;
-      }
+      for (int g = 0; g < kWarpRows; ++g) t += sums[(g * N + n) * 32 + me];
+      if (column(n) < p.cols) part[column(n)] = t;
     }
   } else {
-    float* part = p.part + blockIdx.x * p.cols;
 #pragma unroll
     for (int n = 0; n < N; n += 4) {
       if (VEC) {
@@ -535,17 +459,8 @@ GradPlan grad_plan(int64_t rows, int64_t cols, int elem) {
 }
 
 template <typename T, int NV, bool VEC, bool WARP>
-dbf_status launch_grad_kernel(const NormGradArgs& a, const GradPlan& g, const DeviceInfo& dev, cudaStream_t stream) {
-  auto kernel = dbf_rmsnorm_grad_kernel<T, NV, VEC, WARP>;
-  const size_t sums = WARP ? sizeof(float) * kWarpRows * NV * kChunk * 32 : 0;
-  const size_t smem = std::max(sums, VEC ? sizeof(Pack16<T>) * kDepth<T, NV, WARP> * kGradRows<T, NV> * 3 * NV * g.threads : size_t{0});
-  static std::once_flag once[64];  // the attribute once per device
-  static cudaError_t attr_err[64];
-  std::call_once(once[dev.device], [&] {
-    attr_err[dev.device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
-  });
-  if (attr_err[dev.device] != cudaSuccess) return DBF_ERR_CUDA;
-  return launch_pdl(kernel, dim3(g.blocks), dim3(g.threads), smem, stream, a);
+dbf_status launch_grad_kernel(const NormGradArgs& a, const GradPlan& g, cudaStream_t stream) {
+  return launch_pdl(dbf_rmsnorm_grad_kernel<T, NV, VEC, WARP>, dim3(g.blocks), dim3(g.threads), 0, stream, a);
 }
 
 template <typename T, bool VEC>
@@ -553,26 +468,19 @@ dbf_status launch_grad(NormGradArgs a, const DeviceInfo& dev, cudaStream_t strea
   const GradPlan g = grad_plan(a.rows, a.cols, sizeof(T));
   a.blocks = g.blocks;
   const dbf_status st = g.nv == 0              ? launch_pdl(dbf_rmsnorm_grad_wide_kernel<T>, dim3(g.blocks), dim3(g.threads), 0, stream, a)
-                        : g.warp && g.nv == 1 ? launch_grad_kernel<T, 1, VEC, true>(a, g, dev, stream)
-                        : g.warp              ? launch_grad_kernel<T, 2, VEC, true>(a, g, dev, stream)
+                        : g.warp && g.nv == 1 ? launch_grad_kernel<T, 1, VEC, true>(a, g, stream)
+                        : g.warp              ? launch_grad_kernel<T, 2, VEC, true>(a, g, stream)
                         : g.nv == 1 || sizeof(T) == 4
-                            ? launch_grad_kernel<T, 1, VEC, false>(a, g, dev, stream)
-                            : launch_grad_kernel<T, sizeof(T) == 4 ? 1 : 2, VEC, false>(a, g, dev, stream);
+                            ? launch_grad_kernel<T, 1, VEC, false>(a, g, stream)
+                            : launch_grad_kernel<T, sizeof(T) == 4 ? 1 : 2, VEC, false>(a, g, stream);
   if (st != DBF_OK) return st;
-  // the same division of shared memory and L1 as the kernel before: a change
-  // between two kernels keeps the second from starting beside the first
-  static std::once_flag once[64];
-  std::call_once(once[dev.device], [&] {
-    (void)cudaFuncSetAttribute(dbf_rmsnorm_grad_sum_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                               cudaSharedmemCarveoutMaxShared);
-  });
   return launch_pdl(dbf_rmsnorm_grad_sum_kernel, dim3(static_cast<unsigned>((a.cols + 31) / 32)), dim3(32 * kSumRuns), 0, stream,
                     a);
 }
 
 template <typename T>
 dbf_status grad_typed(const NormGradArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
-  const bool vec = a.cols % kChunk == 0 && aligned_to(a.dy, 16) && aligned_to(a.h, 16) && aligned_to(a.dh, 16) &&
+  const bool vec = a.cols % kChunk == 0 && aligned_to(a.dy, 32) && aligned_to(a.h, 32) && aligned_to(a.dh, 32) &&
                    aligned_to(a.weight, 32) && aligned_to(a.dx, 32);
   return vec ? launch_grad<T, true>(a, dev, stream) : launch_grad<T, false>(a, dev, stream);
 }
