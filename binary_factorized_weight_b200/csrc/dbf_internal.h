@@ -160,21 +160,31 @@ inline dbf_status launch_plain(void (*kernel)(KArgs...), dim3 grid, dim3 block, 
 
 // Launch with programmatic stream serialization: the kernel may be scheduled
 // once its predecessor on the stream has triggered, and waits for it itself
-// (griddepcontrol.wait) before it touches memory.
+// (griddepcontrol.wait) before it touches memory.  cluster: blocks (along x) of
+// a cluster.
 template <typename... KArgs, typename... Args>
-inline dbf_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                             Args... args) {
+inline dbf_status launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                                     int cluster, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...) == cudaSuccess ? DBF_OK : DBF_ERR_CUDA;
+}
+template <typename... KArgs, typename... Args>
+inline dbf_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                             Args... args) {
+  return launch_pdl_cluster(kernel, grid, block, smem, stream, 1, args...);
 }
 
 // ---------------------------------------------------------------- MX operands and dense rows

@@ -224,26 +224,35 @@ __device__ __forceinline__ void row_sums(float (&v)[M], float* red) {
   }
 }
 
-// A row is the work of one warp (WARP, eight rows to a block) or of a block;
-// NV * 16 columns per thread, whose sums of dweight over the rows stay in
-// registers and go to the block's row of `part`.
+// A row is the work of one warp (SPAN 0, eight rows to a block), of a block
+// (SPAN 1) or of a cluster of blocks (SPAN 2, which exchange their sums through
+// distributed shared memory); sixteen columns per thread, whose sums of dweight
+// over the rows stay in registers and go to the row of `part`.
 // VEC: a thread owns sixteen neighbouring columns (32-byte accesses); else every
 // threads-th column.  PRE: the next row is loaded while this one is reduced (16-
-// bit elements, sixteen to a thread: more does not fit the registers).
+// bit elements: more does not fit the registers).
 constexpr int kGradThreads = 512;
-template <typename T, int NV, bool VEC, bool WARP>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kGradThreads, WARP ? 2 : 1)
+template <typename T, bool VEC, int SPAN>
+__global__ void __launch_bounds__(SPAN == 0 ? 32 * kWarpRows : kGradThreads, SPAN == 0 ? 2 : 1)
     dbf_rmsnorm_grad_kernel(const NormGradArgs p) {
-  constexpr int N = NV * kChunk;
-  constexpr bool PRE = NV * sizeof(T) == 2;
+  constexpr int NV = 1, N = kChunk;
+  constexpr bool PRE = sizeof(T) == 2, WARP = SPAN == 0;
   __shared__ float red[2][64];
   __shared__ float sums[WARP ? kWarpRows * N * 32 : 1];
+  __shared__ float2 ranks[SPAN == 2 ? 2 : 1][8];  // the cluster's sums of a row
   pdl_wait();
   pdl_launch_dependents();
-  const int me = WARP ? threadIdx.x & 31 : threadIdx.x, threads = WARP ? 32 : blockDim.x;
+  const int ks = SPAN == 2 ? static_cast<int>(cluster_size()) : 1;
+  const int rank = SPAN == 2 ? static_cast<int>(cluster_rank()) : 0;
+  if constexpr (SPAN == 2) {  // peers write here once every block has started
+    cluster_arrive_relaxed();
+    cluster_wait_acquire();
+  }
+  const int me = WARP ? threadIdx.x & 31 : rank * blockDim.x + threadIdx.x, threads = WARP ? 32 : ks * blockDim.x;
   const int group = WARP ? threadIdx.x >> 5 : 0;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * (WARP ? kWarpRows : 1) + group;
-  const int64_t row_step = static_cast<int64_t>(gridDim.x) * (WARP ? kWarpRows : 1);
+  const int block = blockIdx.x / ks, blocks = gridDim.x / ks;  // a cluster counts as one
+  const int64_t row0 = static_cast<int64_t>(block) * (WARP ? kWarpRows : 1) + group;
+  const int64_t row_step = static_cast<int64_t>(blocks) * (WARP ? kWarpRows : 1);
   // column of this thread's element n
   auto column = [&](int n) -> int64_t {
     return VEC ? kChunk * (me + static_cast<int64_t>(n / kChunk) * threads) + n % kChunk
@@ -301,6 +310,20 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kGradThreads, WARP ? 2
     const float2 th = f2_get(hh), tg = f2_get(gh);
     float s[2] = {th.x + th.y, tg.x + tg.y};
     row_sums<WARP, 2>(s, red[flip]);
+    if constexpr (SPAN == 2) {
+      if (threadIdx.x < ks) {
+        const uint32_t to = map_to_rank(&ranks[flip][rank], threadIdx.x);
+        st_cluster_f32(to, s[0]);
+        st_cluster_f32(to + 4, s[1]);
+      }
+      cluster_arrive_release();
+      cluster_wait_acquire();
+      s[0] = s[1] = 0.f;
+      for (int k = 0; k < ks; ++k) {
+        s[0] += ranks[flip][k].x;
+        s[1] += ranks[flip][k].y;
+      }
+    }
     const float rstd = 1.f / sqrtf(s[0] * inv_cols + p.eps);
     const float c = -(rstd * rstd * rstd * (s[1] * inv_cols));
     const F2 rstd2 = f2(rstd, rstd), c2 = f2(c, c);
@@ -340,7 +363,7 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : kGradThreads, WARP ? 2
     const float2 t = f2_get(dw[n]);
     dws[2 * n] = t.x, dws[2 * n + 1] = t.y;
   }
-  float* part = p.part + blockIdx.x * p.cols;
+  float* part = p.part + block * p.cols;
   if constexpr (WARP) {
     // the block's warps in their order
 #pragma unroll
@@ -436,43 +459,37 @@ __global__ void __launch_bounds__(32 * kSumRuns) dbf_rmsnorm_grad_sum_kernel(con
 // dweight's order of additions follow from it).
 constexpr int kGradSms = 148;
 struct GradPlan {
-  bool warp;    // a row is one warp's work
-  int nv;       // chunks of sixteen columns per thread; 0: the wide kernel
+  int span;     // a row is the work of 0: a warp, 1: a block, 2: a cluster, 3: a block, any width
+  int ks;       // blocks of a cluster
   int threads;  // of a block
   int blocks;   // rows of `part`
 };
-GradPlan grad_plan(int64_t rows, int64_t cols, int elem) {
+GradPlan grad_plan(int64_t rows, int64_t cols) {
   const int64_t chunks = (cols + kChunk - 1) / kChunk;
-  GradPlan g{};
-  g.warp = chunks <= 64;
-  if (g.warp) {
-    g.nv = chunks <= 32 ? 1 : 2;
-    g.threads = 32 * kWarpRows;
-    g.blocks = static_cast<int>(std::min<int64_t>((rows + kWarpRows - 1) / kWarpRows, 2 * kGradSms));
-    return g;
-  }
-  g.nv = chunks <= kGradThreads ? 1 : chunks <= 2 * kGradThreads && elem == 2 ? 2 : 0;
-  g.threads = g.nv ? static_cast<int>(((chunks + g.nv - 1) / g.nv + 31) / 32 * 32) : 1024;
-  const int per_sm = g.nv == 0 ? 2 : g.nv == 2 || g.threads > 256 ? 1 : g.threads > 128 ? 2 : 4;
-  g.blocks = static_cast<int>(std::min<int64_t>(rows, int64_t{kGradSms} * per_sm));
-  return g;
-}
-
-template <typename T, int NV, bool VEC, bool WARP>
-dbf_status launch_grad_kernel(const NormGradArgs& a, const GradPlan& g, cudaStream_t stream) {
-  return launch_pdl(dbf_rmsnorm_grad_kernel<T, NV, VEC, WARP>, dim3(g.blocks), dim3(g.threads), 0, stream, a);
+  auto count = [&](int64_t units, int most) { return static_cast<int>(std::min<int64_t>(units, most)); };
+  if (chunks <= 32) return {0, 1, 32 * kWarpRows, count((rows + kWarpRows - 1) / kWarpRows, 2 * kGradSms)};
+  const int ks = chunks <= kGradThreads ? 1 : chunks <= 2 * kGradThreads ? 2 : chunks <= 4 * kGradThreads ? 4 : 8;
+  if (chunks > 8 * kGradThreads) return {3, 1, 1024, count(rows, 2 * kGradSms)};
+  const int threads = static_cast<int>(((chunks + ks - 1) / ks + 31) / 32 * 32);
+  if (ks > 1) return {2, ks, threads, count(rows, kGradSms / ks)};
+  return {1, 1, threads, count(rows, kGradSms * std::min(kGradThreads / threads, 8))};
 }
 
 template <typename T, bool VEC>
 dbf_status launch_grad(NormGradArgs a, const DeviceInfo& dev, cudaStream_t stream) {
-  const GradPlan g = grad_plan(a.rows, a.cols, sizeof(T));
+  const GradPlan g = grad_plan(a.rows, a.cols);
   a.blocks = g.blocks;
-  const dbf_status st = g.nv == 0              ? launch_pdl(dbf_rmsnorm_grad_wide_kernel<T>, dim3(g.blocks), dim3(g.threads), 0, stream, a)
-                        : g.warp && g.nv == 1 ? launch_grad_kernel<T, 1, VEC, true>(a, g, stream)
-                        : g.warp              ? launch_grad_kernel<T, 2, VEC, true>(a, g, stream)
-                        : g.nv == 1 || sizeof(T) == 4
-                            ? launch_grad_kernel<T, 1, VEC, false>(a, g, stream)
-                            : launch_grad_kernel<T, sizeof(T) == 4 ? 1 : 2, VEC, false>(a, g, stream);
+  const dim3 grid(static_cast<unsigned>(g.blocks * g.ks)), block(g.threads);
+  dbf_status st;
+  if (g.span == 0) {
+    st = launch_pdl(dbf_rmsnorm_grad_kernel<T, VEC, 0>, grid, block, 0, stream, a);
+  } else if (g.span == 1) {
+    st = launch_pdl(dbf_rmsnorm_grad_kernel<T, VEC, 1>, grid, block, 0, stream, a);
+  } else if (g.span == 2) {
+    st = launch_pdl_cluster(dbf_rmsnorm_grad_kernel<T, VEC, 2>, grid, block, 0, stream, g.ks, a);
+  } else {
+    st = launch_pdl(dbf_rmsnorm_grad_wide_kernel<T>, grid, block, 0, stream, a);
+  }
   if (st != DBF_OK) return st;
   return launch_pdl(dbf_rmsnorm_grad_sum_kernel, dim3(static_cast<unsigned>((a.cols + 31) / 32)), dim3(32 * kSumRuns), 0, stream,
                     a);
@@ -537,8 +554,7 @@ dbf_status dbf_rmsnorm_mx_forward(const void* x, const void* residual, const voi
 
 size_t dbf_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols) {
   if (!norm_shape_ok(rows, cols)) return 0;
-  const int blocks = std::max(grad_plan(rows, cols, 2).blocks, grad_plan(rows, cols, 4).blocks);
-  return static_cast<size_t>(blocks) * static_cast<size_t>(cols) * 4;
+  return static_cast<size_t>(grad_plan(rows, cols).blocks) * static_cast<size_t>(cols) * 4;
 }
 
 dbf_status dbf_rmsnorm_backward(const void* dy, const void* h, const void* weight, const void* dh, dbf_dtype t,

@@ -19,7 +19,8 @@ U = 2.0 ** -24
 EPS = 1e-5
 TINY = {"fp16": 2.0 ** -25, "bf16": 2.0 ** -134, "fp32": 2.0 ** -150}  # half the smallest step
 SHAPES = [(1, 1), (1, 32), (2, 64), (3, 100), (1, 4096), (5, 4097), (200, 256), (129, 1000), (17, 8192), (4, 8200),
-          (3, 16384), (2, 16385), (2, 40000), (1000, 512)]
+          (3, 16384), (2, 16385), (2, 40000), (1000, 512),
+          (3, 65536), (2, 65537), (300, 700), (80, 9008)]
 
 
 def rel(cols):
