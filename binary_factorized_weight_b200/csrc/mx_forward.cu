@@ -60,7 +60,7 @@ struct Cfg {
   static constexpr int kStageBytes = kPBytes + kQBytes + kScaleBytes;
   // the epilogue's area: the partial sums of a split tile, or the four warps'
   // 32 x 33 transposes
-  static constexpr int kEpiBytes = WROWS ? NT * kRows * 4 : 4 * 32 * 33 * 4;
+  static constexpr int kEpiBytes = WROWS ? (NT < 32 ? 32 : NT) * kRows * 4 : 4 * 32 * 33 * 4;
   static constexpr int kRoom = 227 * 1024 - 1024 - 512 - kEpiBytes;
   static constexpr int kStages = kRoom / kStageBytes < 8 ? kRoom / kStageBytes : 8;
   static constexpr int kEpiOffset = kStages * kStageBytes;
@@ -251,26 +251,38 @@ __global__ void __launch_bounds__(kThreads, 1)
               store_out(a.out, a.out_t, (q0 + c + j) * a.ld_out + p_row, __uint_as_float(v[j]));
         }
       } else {
-        const int per = (tokens + ks - 1) / ks;  // tokens of a rank, at most
+        // four tokens a store; token group g belongs to rank g % ks (ks a power
+        // of two), which finds rank src's part at [src][g / ks][row]
+        const int lg = 31 - __clz(ks), groups = (tokens + 3) / 4, per = (groups + ks - 1) >> lg;
+        float4* parts = reinterpret_cast<float4*>(epi) + q * 32 + lane;
+        const uint32_t mine = smem_u32(parts + (rank * per) * kRows);
         cluster_wait_acquire();
         for (int c = 0; c < tokens && ok; c += 16) {
           uint32_t v[16];
           tmem_ld_32x32b_x16(acc + c, v);
           tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int t = c + j;
-            if (t < tokens)
-              st_cluster_f32(map_to_rank(epi + (rank * per + t / ks) * kRows + q * 32 + lane, t % ks),
-                             __uint_as_float(v[j]));
+          for (int j = 0; j < 16; j += 4) {
+            const int g = (c + j) >> 2;
+            if (g < groups)
+              st_cluster_v4f32(cluster_addr(mine + (g >> lg) * (kRows * 16), g & (ks - 1)), __uint_as_float(v[j]),
+                               __uint_as_float(v[j + 1]), __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
           }
         }
         cluster_arrive_release();
         cluster_wait_acquire();
-        for (int t = rank; t < tokens && ok; t += ks) {
-          float sum = 0.f;
-          for (int src = 0; src < ks; ++src) sum += epi[(src * per + t / ks) * kRows + q * 32 + lane];
-          if (p_row < a.p_rows) store_out(a.out, a.out_t, (q0 + t) * a.ld_out + p_row, sum);
+        for (int g = rank; g < groups && ok; g += ks) {
+          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int src = 0; src < ks; ++src) {
+            const float4 t = parts[(src * per + (g >> lg)) * kRows];
+            sum.x += t.x, sum.y += t.y, sum.z += t.z, sum.w += t.w;
+          }
+          if (p_row < a.p_rows) {
+            const float out[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (4 * g + j < tokens) store_out(a.out, a.out_t, (q0 + 4 * g + j) * a.ld_out + p_row, out[j]);
+          }
         }
       }
     } else {
