@@ -511,15 +511,19 @@ template <int N>
 __device__ __forceinline__ void bulk_wait_all() {
   asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory");
 }
-// Bounded wait on a barrier that the pair's other CTA arrives on too.
-__device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
-  if (mbar_try_wait_acq_cluster(bar, parity)) return true;
-  const unsigned long long t0 = globaltimer_ns();
+// Bounded waits for loops that wait every few hundred cycles: the clock is read
+// only after 64 failed tries (reading it costs more than such a wait lasts).
+// CLUSTER: another CTA arrives on the barrier too.
+template <bool CLUSTER>
+__device__ __forceinline__ bool mbar_wait_often(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  unsigned long long t0 = 0;
   for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait_acq_cluster(bar, parity)) return true;
+    if (CLUSTER ? mbar_try_wait_acq_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
     if ((it & 63u) == 0) {
       if (*abort_flag) return false;
-      if (globaltimer_ns() - t0 > kWaitBudgetNs) {
+      const unsigned long long t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitBudgetNs) {
         *abort_flag = 1;
         if (status) atomicCAS(status, 0, kStatusTimeout);
         return false;

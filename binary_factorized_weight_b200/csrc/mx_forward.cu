@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int it = early;
       for (; kt0 + it < kt1; ++it) {
         const int s = it % S;
-        if (!mbar_wait_bounded(&empty[s], (it / S - 1) & 1, abort_flag, a.status)) break;
+        if (!mbar_wait_often<false>(&empty[s], (it / S - 1) & 1, abort_flag, a.status)) break;
         expect(kt0 + it, s);
         load_p(kt0 + it, s);
         load_q(kt0 + it, s);
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // after a wait that gave up: no copy may still be on its way when the CTA ends
       if (*abort_flag) {
         int never = 0;
-        for (int i = max(0, it - S); i < it; ++i) (void)mbar_wait_bounded(&full[i % S], (i / S) & 1, &never, a.status);
+        for (int i = max(0, it - S); i < it; ++i) (void)mbar_wait_often<false>(&full[i % S], (i / S) & 1, &never, a.status);
       }
     }
   } else if (warp == 1) {
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int kt = kt0, it = 0; kt < kt1; ++kt, ++it) {
         const int s = it % S;
-        if (!mbar_wait_bounded(&full[s], (it / S) & 1, abort_flag, a.status)) {
+        if (!mbar_wait_often<false>(&full[s], (it / S) & 1, abort_flag, a.status)) {
           ok = false;
           break;
         }
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------ epilogue
     const int q = warp & 3;  // the TMEM lanes this warp may read
-    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_full, 0, abort_flag, a.status));
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_often<false>(acc_full, 0, abort_flag, a.status));
     tc_fence_after();
     const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const int64_t p_row = p0 + q * 32 + lane;
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    (void)mbar_wait_bounded(mma_done, 0, abort_flag, a.status);
+    (void)mbar_wait_often<false>(mma_done, 0, abort_flag, a.status);
     __syncwarp();
     tmem_dealloc(tmem, C::kTmemCols);
   }
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t q0 = (t / p_tiles) * NT;
         for (int kt = 0; kt < a.stages_k; ++kt, ++it) {
           const int s = static_cast<int>(it % S);
-          if (it >= S && !mbar_wait_pair(&empty[s], (it / S - 1) & 1, abort_flag, a.status)) {
+          if (it >= S && !mbar_wait_often<true>(&empty[s], (it / S - 1) & 1, abort_flag, a.status)) {
             ok = false;
             break;
           }
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (*abort_flag && rank == 0) {
         int never = 0;
         for (uint32_t i = it < S ? 0 : it - S; i < it; ++i)
-          (void)mbar_wait_pair(&full[i % S], (i / S) & 1, &never, a.status);
+          (void)mbar_wait_often<true>(&full[i % S], (i / S) & 1, &never, a.status);
       }
     }
   } else if (warp == 1) {
@@ -482,20 +482,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t b = n & 1, use = n >> 1;
         // this accumulator's last tile has been read, and the tile before has
         // left the shared columns
-        if (n >= 2) ok = mbar_wait_pair(&acc_empty[b], (use - 1) & 1, abort_flag, a.status);
+        if (n >= 2) ok = mbar_wait_often<true>(&acc_empty[b], (use - 1) & 1, abort_flag, a.status);
         if (C::kShared > 0 && n >= 1 && ok)
-          ok = mbar_wait_pair(&acc_shared[b ^ 1], ((n - 1) >> 1) & 1, abort_flag, a.status);
+          ok = mbar_wait_often<true>(&acc_shared[b ^ 1], ((n - 1) >> 1) & 1, abort_flag, a.status);
         if (!ok) break;
         const uint32_t d = tmem + b * C::kAcc1;
         // where the tile's first weight row lies in its scale tile
         const uint32_t q_col = static_cast<uint32_t>(((t / p_tiles) * NT & 127) >> 5);
         for (int kt = 0; kt < a.stages_k; ++kt, ++it) {
           const int s = static_cast<int>(it % S);
-          ok = mbar_wait_pair(&full[s], (it / S) & 1, abort_flag, a.status);
+          ok = mbar_wait_often<true>(&full[s], (it / S) & 1, abort_flag, a.status);
           // the MMAs that read this stage's scale buffer before have completed
           if (ok && it >= C::kScaleBufs) {
             const uint32_t old = it - C::kScaleBufs;
-            ok = mbar_wait_pair(&empty[old % S], (old / S) & 1, abort_flag, a.status);
+            ok = mbar_wait_often<true>(&empty[old % S], (old / S) & 1, abort_flag, a.status);
           }
           if (!ok) break;
           tc_fence_after();
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t n = 0, stores = 0;
     for (int64_t t = pair; t < tiles; t += pairs, ++n) {
       const uint32_t b = n & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait_pair(&acc_full[b], (n >> 1) & 1, abort_flag, a.status))) break;
+      if (!__all_sync(0xffffffffu, mbar_wait_often<true>(&acc_full[b], (n >> 1) & 1, abort_flag, a.status))) break;
       tc_fence_after();
       const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * C::kAcc1;
       const int64_t row0 = (t % p_tiles) * 256 + rank * kRows + q * 32, q0 = (t / p_tiles) * NT;
@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ------------------------------------------------ teardown
   __syncwarp();
   tc_fence_before();
-  if (warp == 1) (void)mbar_wait_pair(mma_done, 0, abort_flag, a.status);
+  if (warp == 1) (void)mbar_wait_often<true>(mma_done, 0, abort_flag, a.status);
   // neither CTA ends while the other may still read its memory or signal it
   cluster_arrive_release();
   cluster_wait_acquire();
