@@ -7,17 +7,11 @@
 // widened to a byte per element by the TMA copy) and applies the scales of both
 // operands itself, from tensor memory.  Sums are fp32.
 //
-// A tile is 128 rows of one operand (P, the tensor cores' M) by NT of the other
-// (Q, their N).  A stage of the shared-memory ring is 128 bytes of every row:
-// 256 4-bit or 128 byte-wide elements of K, with the 512-byte scale tiles (128
-// rows x 128 elements) that belong to them.
-//
-// Roles (192 threads): warp 0 TMA producer; warp 1 tensor memory and the
-// single-thread issue of scale copies and MMAs; warps 2-5 epilogue.
-//
-// Few tiles (WROWS: P = the weight's rows, Q = the tokens, NT small): the K range
-// of a tile is split over a cluster, each CTA sends its fp32 partial of token t
-// to CTA t % size, which adds them in rank order.
+// Both kernels fill a shared-memory ring by TMA in steps of 128 bytes of every
+// row: 256 4-bit or 128 byte-wide elements of K, with the 512-byte scale tiles
+// (128 rows x 128 elements) that belong to them.  tcgen05.cp brings those into
+// tensor memory.  Roles (192 threads): warp 0 TMA producer; warp 1 tensor memory
+// and the single-thread issue of scale copies and MMAs; warps 2-5 epilogue.
 //
 // Every wait is bounded; one that gives up records DBF_ERR_TIMEOUT in the
 // workspace's status word and the kernel ends with y incomplete.
@@ -41,37 +35,14 @@ struct MxArgs {
   const uint8_t* q_scales;
   int64_t p_rows, q_rows;
   int64_t k4s;       // 128-element groups of K (scale tiles in a row of tiles)
-  int stages_k;      // stages of the whole K range
+  int steps_k;       // steps (128 bytes of a row) of the whole K range
   int p_tx, q_tx;    // bytes that a row of P, Q counts on its barrier
   uint32_t idesc;
-  int p_static;      // P (WROWS) or Q holds weights that may be read before the PDL wait
+  int w_static;      // the weights may be read before the PDL wait
   void* out;
   int64_t ld_out;
   int out_t;
   int* status;
-};
-
-template <int KA, int NT, bool WROWS>
-struct Cfg {
-  static constexpr int kQTiles = (NT + 127) / 128;  // scale tiles of Q's rows
-  static constexpr int kPBytes = kRows * kRowBytes;
-  static constexpr int kQBytes = NT * kRowBytes;
-  static constexpr int kScaleBytes = KA * (1 + kQTiles) * kTileBytes;
-  static constexpr int kStageBytes = kPBytes + kQBytes + kScaleBytes;
-  // the epilogue's area: the partial sums of a split tile, or the four warps'
-  // 32 x 33 transposes
-  static constexpr int kEpiBytes = WROWS ? (NT < 32 ? 32 : NT) * kRows * 4 : 4 * 32 * 33 * 4;
-  static constexpr int kRoom = 227 * 1024 - 1024 - 512 - kEpiBytes;
-  static constexpr int kStages = kRoom / kStageBytes < 8 ? kRoom / kStageBytes : 8;
-  static constexpr int kEpiOffset = kStages * kStageBytes;
-  static constexpr int kBarOffset = kEpiOffset + kEpiBytes;
-  static constexpr int kSmemBytes = kBarOffset + 512 + 1024;
-  static constexpr int kScaleCols = KA * 4 * (1 + kQTiles);
-  static constexpr int kDCols = NT < 32 ? 32 : NT;
-  static constexpr int kNeedCols = kDCols + kStages * kScaleCols;
-  static constexpr int kTmemCols = kNeedCols <= 128 ? 128 : kNeedCols <= 256 ? 256 : 512;
-  static_assert(kNeedCols <= 512, "accumulator and scales must fit in tensor memory");
-  static_assert(kStages >= 2, "");
 };
 
 __device__ __forceinline__ void store_out(void* out, int t, int64_t at, float v) {
@@ -84,18 +55,48 @@ __device__ __forceinline__ void store_out(void* out, int t, int64_t at, float v)
   }
 }
 
-template <int KA, int NT, bool WROWS>
+// ---------------------------------------------------------------- few tiles: K split over a cluster
+// Tiles of 128 weight rows (the tensor cores' M) by NT tokens (their N; up to NT
+// tokens read as zero).  The K range of a tile is split over the CTAs of a
+// cluster, each of which sends its fp32 partial sums of token group g to CTA
+// g % size, which adds them in rank order.  With few tokens the weights'
+// stream bounds it; a stage of the ring is U steps, because a stage costs some
+// 250 cycles of waiting and signalling however little it multiplies.
+template <int KA, int NT>
+struct SplitCfg {
+  static constexpr int U = NT <= 32 ? 2 : 1;
+  static constexpr int kPBytes = kRows * kRowBytes;  // of a step
+  static constexpr int kQBytes = NT * kRowBytes;
+  static constexpr int kScaleBytes = U * KA * kTileBytes;  // of a stage and operand
+  static constexpr int kStageBytes = U * (kPBytes + kQBytes) + 2 * kScaleBytes;
+  static constexpr int kEpiBytes = (NT < 32 ? 32 : NT) * kRows * 4;  // the partial sums of the cluster
+  static constexpr int kRoom = 227 * 1024 - 1024 - 512 - kEpiBytes;
+  static constexpr int kStages = kRoom / kStageBytes < 8 ? kRoom / kStageBytes : 8;
+  static constexpr int kEpiOffset = kStages * kStageBytes;
+  static constexpr int kBarOffset = kEpiOffset + kEpiBytes;
+  static constexpr int kSmemBytes = kBarOffset + 512 + 1024;
+  // tensor memory: the accumulator, then each stage's scales (a copy may
+  // overtake earlier MMAs, so a stage's place is its own as long as its slot of the ring is)
+  static constexpr int kScaleCols = 2 * 4 * KA * U;
+  static constexpr int kDCols = NT < 32 ? 32 : NT;
+  static constexpr int kNeedCols = kDCols + kStages * kScaleCols;
+  static constexpr int kTmemCols = kNeedCols <= 128 ? 128 : kNeedCols <= 256 ? 256 : 512;
+  static_assert(kNeedCols <= 512, "accumulator and scales must fit in tensor memory");
+  static_assert(kStages >= 2, "");
+};
+
+template <int KA, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
-    dbf_mx_gemm_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
-                       const MxArgs a) {
-  using C = Cfg<KA, NT, WROWS>;
-  constexpr int S = C::kStages;
+    dbf_mx_gemm_split_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
+                             const MxArgs a) {
+  using C = SplitCfg<KA, NT>;
+  constexpr int S = C::kStages, U = C::U;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   // operand rings first: their 128-byte swizzle counts from 1024-byte boundaries
   uint8_t* p_st = smem;
-  uint8_t* q_st = smem + S * C::kPBytes;
-  uint8_t* s_st = q_st + S * C::kQBytes;
+  uint8_t* q_st = smem + S * U * C::kPBytes;
+  uint8_t* s_st = q_st + S * U * C::kQBytes;  // per stage: P's tiles, Q's tiles
   float* epi = reinterpret_cast<float*>(smem + C::kEpiOffset);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
   uint64_t* empty = full + S;
@@ -105,15 +106,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int ks = WROWS ? static_cast<int>(cluster_size()) : 1;
-  const int rank = WROWS ? static_cast<int>(cluster_rank()) : 0;
+  const int ks = static_cast<int>(cluster_size());
+  const int rank = static_cast<int>(cluster_rank());
   const int64_t p_tiles = (a.p_rows + kRows - 1) / kRows;
   const int64_t tile = blockIdx.x / ks;
   const int64_t p0 = (tile % p_tiles) * kRows, q0 = (tile / p_tiles) * NT;
-  const int kt0 = static_cast<int>(static_cast<int64_t>(a.stages_k) * rank / ks);
-  const int kt1 = static_cast<int>(static_cast<int64_t>(a.stages_k) * (rank + 1) / ks);
+  // this CTA's steps of K, and stages of U of them
+  const int k0 = static_cast<int>(static_cast<int64_t>(a.steps_k) * rank / ks);
+  const int k1 = static_cast<int>(static_cast<int64_t>(a.steps_k) * (rank + 1) / ks);
+  const int stages = (k1 - k0 + U - 1) / U;
 
   if (tid == 0) {
+    prefetch_tmap(&p_map);
+    prefetch_tmap(&q_map);
     for (int i = 0; i < S; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
@@ -122,8 +127,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_barrier_init();
-    prefetch_tmap(&p_map);
-    prefetch_tmap(&q_map);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, C::kTmemCols);
@@ -134,53 +137,49 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   pdl_launch_dependents();
   // a rank's partial sums are written only after every CTA of its cluster has started
-  if constexpr (WROWS) cluster_arrive_relaxed();
+  cluster_arrive_relaxed();
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer
     if (elect_one()) {
-      // scale tiles of Q's rows that exist (the last tile of rows may stand alone)
-      const int q_tiles = static_cast<int>(min(static_cast<int64_t>(C::kQTiles), (a.q_rows - q0 + 127) >> 7));
-      auto load_p = [&](int kt, int s) {
-        const int atoms = static_cast<int>(min(static_cast<int64_t>(KA), a.k4s - static_cast<int64_t>(kt) * KA));
-        tma_load_2d(p_st + s * C::kPBytes, &p_map, kt * 128, static_cast<int>(p0), &full[s]);
-        bulk_load(s_st + s * C::kScaleBytes, a.p_scales + ((p0 >> 7) * a.k4s + static_cast<int64_t>(kt) * KA) * kTileBytes,
-                  atoms * kTileBytes, &full[s]);
+      auto tiles_of = [&](int k) {  // 128-element groups of the stage that starts at step k
+        return static_cast<int>(min(static_cast<int64_t>(min(U, k1 - k) * KA), a.k4s - static_cast<int64_t>(k) * KA));
       };
-      auto load_q = [&](int kt, int s) {
-        const int atoms = static_cast<int>(min(static_cast<int64_t>(KA), a.k4s - static_cast<int64_t>(kt) * KA));
-        tma_load_2d(q_st + s * C::kQBytes, &q_map, kt * 128, static_cast<int>(q0), &full[s]);
-        for (int j = 0; j < q_tiles; ++j)
-          bulk_load(s_st + s * C::kScaleBytes + KA * (1 + j) * kTileBytes,
-                    a.q_scales + (((q0 >> 7) + j) * a.k4s + static_cast<int64_t>(kt) * KA) * kTileBytes,
-                    atoms * kTileBytes, &full[s]);
+      auto load = [&](bool weights, int i) {
+        const int k = k0 + i * U, s = i % S, tiles = tiles_of(k);
+        const CUtensorMap* map = weights ? &p_map : &q_map;
+        const uint8_t* scales = weights ? a.p_scales : a.q_scales;
+        const int64_t row = weights ? p0 : q0;
+        const int bytes = weights ? C::kPBytes : C::kQBytes;
+        uint8_t* st = (weights ? p_st : q_st) + s * U * bytes;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (u == 0 || k + u < k1) tma_load_2d(st + u * bytes, map, (k + u) * 128, static_cast<int>(row), &full[s]);
+        bulk_load(s_st + (2 * s + (weights ? 0 : 1)) * C::kScaleBytes,
+                  scales + ((row >> 7) * a.k4s + static_cast<int64_t>(k) * KA) * kTileBytes, tiles * kTileBytes, &full[s]);
       };
-      auto expect = [&](int kt, int s) {
-        const int atoms = static_cast<int>(min(static_cast<int64_t>(KA), a.k4s - static_cast<int64_t>(kt) * KA));
-        mbar_arrive_expect_tx(&full[s], kRows * a.p_tx + NT * a.q_tx + (1 + q_tiles) * atoms * kTileBytes);
+      auto expect = [&](int i) {
+        const int k = k0 + i * U;
+        mbar_arrive_expect_tx(&full[i % S],
+                              min(U, k1 - k) * (kRows * a.p_tx + NT * a.q_tx) + 2 * tiles_of(k) * kTileBytes);
       };
       // the first ring's worth of the weights is on its way before the wait for
       // the kernel that writes the tokens
-      const int early = min(S, kt1 - kt0);
-      if (!a.p_static) pdl_wait();
+      const int early = min(S, stages);
+      if (!a.w_static) pdl_wait();
       for (int i = 0; i < early; ++i) {
-        expect(kt0 + i, i);
-        if (WROWS) load_p(kt0 + i, i);
-        else load_q(kt0 + i, i);
+        expect(i);
+        load(true, i);
       }
-      if (a.p_static) pdl_wait();
-      for (int i = 0; i < early; ++i) {
-        if (WROWS) load_q(kt0 + i, i);
-        else load_p(kt0 + i, i);
-      }
+      if (a.w_static) pdl_wait();
+      for (int i = 0; i < early; ++i) load(false, i);
       int it = early;
-      for (; kt0 + it < kt1; ++it) {
-        const int s = it % S;
-        if (!mbar_wait_often<false>(&empty[s], (it / S - 1) & 1, abort_flag, a.status)) break;
-        expect(kt0 + it, s);
-        load_p(kt0 + it, s);
-        load_q(kt0 + it, s);
+      for (; it < stages; ++it) {
+        if (!mbar_wait_often<false>(&empty[it % S], (it / S - 1) & 1, abort_flag, a.status)) break;
+        expect(it);
+        load(true, it);
+        load(false, it);
       }
       // after a wait that gave up: no copy may still be on its way when the CTA ends
       if (*abort_flag) {
@@ -192,38 +191,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------ scale copies and MMAs
     if (elect_one()) {
       bool ok = true;
-      for (int kt = kt0, it = 0; kt < kt1; ++kt, ++it) {
-        const int s = it % S;
+      for (int it = 0; it < stages; ++it) {
+        const int k = k0 + it * U, s = it % S;
         if (!mbar_wait_often<false>(&full[s], (it / S) & 1, abort_flag, a.status)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t sc = smem_u32(s_st + s * C::kScaleBytes);
-        const uint32_t sf = tmem + C::kDCols + s * C::kScaleCols;  // P's, then Q's columns
+        const uint32_t sc = smem_u32(s_st + 2 * s * C::kScaleBytes);
+        const uint32_t sfp = tmem + C::kDCols + s * C::kScaleCols, sfq = sfp + 4 * KA * U;
+        // K behind the last group of 128 elements is not multiplied: it has no scales
+        const int64_t tiles = a.k4s - static_cast<int64_t>(k) * KA;
 #pragma unroll
-        for (int k = 0; k < KA; ++k) {
-          tc_copy_scales(sf + 4 * k, smem_desc_rows16(sc + k * kTileBytes));
-#pragma unroll
-          for (int j = 0; j < C::kQTiles; ++j)
-            tc_copy_scales(sf + 4 * KA + 4 * (k * C::kQTiles + j),
-                           smem_desc_rows16(sc + (KA * (1 + j) + k) * kTileBytes));
+        for (int z = 0; z < KA * U; ++z) {
+          if (z >= KA && k + z / KA >= k1) break;
+          tc_copy_scales(sfp + 4 * z, smem_desc_rows16(sc + z * kTileBytes));
+          tc_copy_scales(sfq + 4 * z, smem_desc_rows16(sc + C::kScaleBytes + z * kTileBytes));
         }
-        const uint32_t pa = smem_u32(p_st + s * C::kPBytes), qa = smem_u32(q_st + s * C::kQBytes);
-        // K behind the last group of 128 is not multiplied: its scales were not copied
-        const bool whole = KA == 1 || a.k4s - static_cast<int64_t>(kt) * KA >= KA;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          if (KA == 2 && kk >= 2 && !whole) break;
-          const uint32_t acc = it != 0 || kk != 0 ? 1u : 0u;
-          const uint64_t pd = smem_desc_sw128_kmajor(pa + kk * 32), qd = smem_desc_sw128_kmajor(qa + kk * 32);
-          if constexpr (KA == 2) {
-            const uint32_t id = 2u * (kk & 1);
-            tc_mma_mxf4(tmem, pd, qd, a.idesc | (id << 4) | (id << 29), sf + 4 * (kk >> 1),
-                        sf + 4 * KA + 4 * C::kQTiles * (kk >> 1), acc);
-          } else {
-            tc_mma_mxf8f6f4(tmem, pd, qd, a.idesc | (static_cast<uint32_t>(kk) << 4) | (static_cast<uint32_t>(kk) << 29),
-                            sf, sf + 4, acc);
+        for (int u = 0; u < U; ++u) {
+          if (u > 0 && k + u >= k1) break;
+          const uint32_t pa = smem_u32(p_st + (s * U + u) * C::kPBytes), qa = smem_u32(q_st + (s * U + u) * C::kQBytes);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if (KA == 2 && kk >= 2 && tiles <= 2 * u + 1) break;
+            const uint32_t acc = it != 0 || u != 0 || kk != 0 ? 1u : 0u;
+            const uint64_t pd = smem_desc_sw128_kmajor(pa + kk * 32), qd = smem_desc_sw128_kmajor(qa + kk * 32);
+            if constexpr (KA == 2) {
+              const uint32_t id = 2u * (kk & 1), at = 4 * (2 * u + (kk >> 1));
+              tc_mma_mxf4(tmem, pd, qd, a.idesc | (id << 4) | (id << 29), sfp + at, sfq + at, acc);
+            } else {
+              tc_mma_mxf8f6f4(tmem, pd, qd,
+                              a.idesc | (static_cast<uint32_t>(kk) << 4) | (static_cast<uint32_t>(kk) << 29), sfp + 4 * u,
+                              sfq + 4 * u, acc);
+            }
           }
         }
         tc_commit(&empty[s]);
@@ -238,85 +239,64 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16);
     const int64_t p_row = p0 + q * 32 + lane;
-    if constexpr (WROWS) {
-      const int tokens = static_cast<int>(min(static_cast<int64_t>(NT), a.q_rows - q0));
-      if (ks == 1) {
-        for (int c = 0; c < tokens && ok; c += 16) {
-          uint32_t v[16];
-          tmem_ld_32x32b_x16(acc + c, v);
-          tmem_ld_wait();
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(NT), a.q_rows - q0));
+    if (ks == 1) {
+      for (int c = 0; c < tokens && ok; c += 16) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(acc + c, v);
+        tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c + j < tokens && p_row < a.p_rows)
-              store_out(a.out, a.out_t, (q0 + c + j) * a.ld_out + p_row, __uint_as_float(v[j]));
-        }
-      } else {
-        // four tokens a store; token group g belongs to rank g % ks (ks a power
-        // of two), which finds rank src's part at [src][g / ks][row]
-        const int lg = 31 - __clz(ks), groups = (tokens + 3) / 4, per = (groups + ks - 1) >> lg;
-        float4* parts = reinterpret_cast<float4*>(epi) + q * 32 + lane;
-        const uint32_t mine = smem_u32(parts + (rank * per) * kRows);
-        cluster_wait_acquire();
-        for (int c = 0; c < tokens && ok; c += 16) {
-          uint32_t v[16];
-          tmem_ld_32x32b_x16(acc + c, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const int g = (c + j) >> 2;
-            if (g < groups)
-              st_cluster_v4f32(cluster_addr(mine + (g >> lg) * (kRows * 16), g & (ks - 1)), __uint_as_float(v[j]),
-                               __uint_as_float(v[j + 1]), __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
-          }
-        }
-        cluster_arrive_release();
-        cluster_wait_acquire();
-        for (int g = rank; g < groups && ok; g += ks) {
-          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int src = 0; src < ks; ++src) {
-            const float4 t = parts[(src * per + (g >> lg)) * kRows];
-            sum.x += t.x, sum.y += t.y, sum.z += t.z, sum.w += t.w;
-          }
-          if (p_row < a.p_rows) {
-            const float out[4] = {sum.x, sum.y, sum.z, sum.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (4 * g + j < tokens) store_out(a.out, a.out_t, (q0 + 4 * g + j) * a.ld_out + p_row, out[j]);
-          }
-        }
+        for (int j = 0; j < 16; ++j)
+          if (c + j < tokens && p_row < a.p_rows)
+            store_out(a.out, a.out_t, (q0 + c + j) * a.ld_out + p_row, __uint_as_float(v[j]));
       }
     } else {
-      float* st = epi + q * 32 * 33;
-      const int64_t row0 = p0 + q * 32;
-      const int rows = static_cast<int>(max(int64_t{0}, min(int64_t{32}, a.p_rows - row0)));
-      for (int c = 0; c < NT && ok; c += 32) {
-        if (q0 + c >= a.q_rows) break;
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(acc + c, v);
+      // four tokens a store; token group g belongs to rank g % ks (ks a power
+      // of two), which finds rank src's part at [src][g / ks][row]
+      const int lg = 31 - __clz(ks), groups = (tokens + 3) / 4, per = (groups + ks - 1) >> lg;
+      float4* parts = reinterpret_cast<float4*>(epi) + q * 32 + lane;
+      const uint32_t mine = smem_u32(parts + (rank * per) * kRows);
+      cluster_wait_acquire();
+      for (int c = 0; c < tokens && ok; c += 16) {
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(acc + c, v);
         tmem_ld_wait();
-        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) st[lane * 33 + j] = __uint_as_float(v[j]);
-        __syncwarp();
-        const int64_t col = q0 + c + lane;
-        if (col < a.q_rows)
-          for (int r = 0; r < rows; ++r) store_out(a.out, a.out_t, (row0 + r) * a.ld_out + col, st[r * 33 + lane]);
+        for (int j = 0; j < 16; j += 4) {
+          const int g = (c + j) >> 2;
+          if (g < groups)
+            st_cluster_v4f32(cluster_addr(mine + (g >> lg) * (kRows * 16), g & (ks - 1)), __uint_as_float(v[j]),
+                             __uint_as_float(v[j + 1]), __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+        }
+      }
+      cluster_arrive_release();
+      cluster_wait_acquire();
+      for (int g = rank; g < groups && ok; g += ks) {
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int src = 0; src < ks; ++src) {
+          const float4 t = parts[(src * per + (g >> lg)) * kRows];
+          sum.x += t.x, sum.y += t.y, sum.z += t.z, sum.w += t.w;
+        }
+        if (p_row < a.p_rows) {
+          const float out[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (4 * g + j < tokens) store_out(a.out, a.out_t, (q0 + 4 * g + j) * a.ld_out + p_row, out[j]);
+        }
       }
     }
   }
 
   // ------------------------------------------------ teardown
-  if constexpr (WROWS) {
-    // every thread takes part in the cluster's barriers: the epilogue's two of a
-    // split tile, or one to pair the first arrival
-    __syncwarp();
-    if (ks == 1) {
-      cluster_wait_acquire();
-    } else if (warp < 2) {
-      cluster_wait_acquire();
-      cluster_arrive_release();
-      cluster_wait_acquire();
-    }
+  // every thread takes part in the cluster's barriers: the epilogue's two of a
+  // split tile, or one to pair the first arrival
+  __syncwarp();
+  if (ks == 1) {
+    cluster_wait_acquire();
+  } else if (warp < 2) {
+    cluster_wait_acquire();
+    cluster_arrive_release();
+    cluster_wait_acquire();
   }
   tc_fence_before();
   __syncthreads();
@@ -347,7 +327,7 @@ struct PairCfg {
   static constexpr int kQBytes = kQRows * kRowBytes;
   static constexpr int kScaleBytes = KA * (1 + kQTiles) * kTileBytes;
   static constexpr int kStageBytes = kPBytes + kQBytes + kScaleBytes;
-  static constexpr int kWarpBuf = 32 * 128;  // 32 rows x 128 bytes
+  static constexpr int kWarpBuf = 32 * 128;  // 32 rows x 32 columns
   static constexpr int kBufs = 3;            // per epilogue warp
   static constexpr int kEpiBytes = 4 * kBufs * kWarpBuf;
   static constexpr int kRoom = 227 * 1024 - 1024 - 512 - kEpiBytes;
@@ -358,8 +338,8 @@ struct PairCfg {
   static constexpr int kSmemBytes = kBarOffset + 512 + 1024;
   // scales in tensor memory: a copy may overtake the MMAs issued before it, so a
   // stage's scales go where no running MMA reads
-  static constexpr int kScaleBufs = 3;
   static constexpr int kScaleCols = 4 * KA * (1 + kQTiles);
+  static constexpr int kScaleBufs = 512 - 2 * NT >= 2 * kScaleCols && 512 - 2 * NT < 3 * kScaleCols ? 2 : 3;
   static constexpr int kScaleBase = 512 - kScaleBufs * kScaleCols;
   static_assert(kStages > kScaleBufs, "a buffer's last stage must still be told from the next one in its place");
   // the second accumulator starts where it still ends before the scales
@@ -371,10 +351,9 @@ struct PairCfg {
 struct PairArgs {
   int64_t p_rows, q_rows;
   int64_t k4s;
-  int stages_k;
+  int steps_k;
   int tx;  // bytes of a stage, both CTAs
   uint32_t idesc;
-  int w_static;
   void* out;
   int64_t ld_out;
   int out_t;
@@ -451,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int64_t t = pair; t < tiles && ok; t += pairs) {
         const int p0 = static_cast<int>((t % p_tiles) * 256) + rank * kRows;
         const int64_t q0 = (t / p_tiles) * NT;
-        for (int kt = 0; kt < a.stages_k; ++kt, ++it) {
+        for (int kt = 0; kt < a.steps_k; ++kt, ++it) {
           const int s = static_cast<int>(it % S);
           if (it >= S && !mbar_wait_often<true>(&empty[s], (it / S - 1) & 1, abort_flag, a.status)) {
             ok = false;
@@ -489,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t d = tmem + b * C::kAcc1;
         // where the tile's first weight row lies in its scale tile
         const uint32_t q_col = static_cast<uint32_t>(((t / p_tiles) * NT & 127) >> 5);
-        for (int kt = 0; kt < a.stages_k; ++kt, ++it) {
+        for (int kt = 0; kt < a.steps_k; ++kt, ++it) {
           const int s = static_cast<int>(it % S);
           ok = mbar_wait_often<true>(&full[s], (it / S) & 1, abort_flag, a.status);
           // the MMAs that read this stage's scale buffer before have completed
@@ -533,7 +512,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------ epilogue
     const int q = warp & 3;  // the TMEM lanes this warp may read
     uint8_t* buf = epi_st + q * (C::kBufs * C::kWarpBuf);
-    const int cols = a.out_t == DBF_F32 ? 32 : 64;  // of 128 bytes
     uint32_t n = 0, stores = 0;
     for (int64_t t = pair; t < tiles; t += pairs, ++n) {
       const uint32_t b = n & 1;
@@ -542,39 +520,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * C::kAcc1;
       const int64_t row0 = (t % p_tiles) * 256 + rank * kRows + q * 32, q0 = (t / p_tiles) * NT;
       const int rows = static_cast<int>(max(int64_t{0}, min(int64_t{32}, a.p_rows - row0)));
-      // the columns shared with the other accumulator first: the last ones of
-      // accumulator 0, the first of accumulator 1
-      for (int i = 0; i < NT / cols; ++i) {
-        const int c0 = b == 0 && C::kShared > 0 ? NT - (i + 1) * cols : i * cols;
-        uint8_t* dst = buf + (stores % C::kBufs) * C::kWarpBuf;
-        uint32_t v[64];
-        uint32_t(&v0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[0]);
-        uint32_t(&v1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[32]);
-        tmem_ld_32x32b_x32(acc + c0, v0);
-        if (cols == 64) tmem_ld_32x32b_x32(acc + c0 + 32, v1);
+      // 32 columns at a time; those shared with the other accumulator first:
+      // the last ones of accumulator 0, the first of accumulator 1
+      for (int i = 0; i < NT / 32; ++i) {
+        const int c0 = b == 0 && C::kShared > 0 ? NT - (i + 1) * 32 : i * 32;
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(acc + c0, v);
         tmem_ld_wait();
-        const bool shared_read = C::kShared > 0 && (i + 1) * cols == (C::kShared + cols - 1) / cols * cols;
-        if (shared_read || i + 1 == NT / cols) {
+        if ((i + 1) * 32 == C::kShared || i + 1 == NT / 32) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            if (shared_read) mbar_arrive_remote_release(map_to_rank(&acc_shared[b], 0));
-            if (i + 1 == NT / cols) mbar_arrive_remote_release(map_to_rank(&acc_empty[b], 0));
+            if ((i + 1) * 32 == C::kShared) mbar_arrive_remote_release(map_to_rank(&acc_shared[b], 0));
+            if (i + 1 == NT / 32) mbar_arrive_remote_release(map_to_rank(&acc_empty[b], 0));
           }
         }
+        uint8_t* dst = buf + (stores % C::kBufs) * C::kWarpBuf;
         // the store that last used this buffer has read it
         if (lane == 0) bulk_wait_read<C::kBufs - 1>();
         __syncwarp();
-        // 16-byte chunk c of row r lies at chunk c ^ (r & 7): the TMA map's swizzle
-        uint8_t* line = dst + lane * 128;
+        // the TMA map's swizzle: of a row's 16-byte chunks, chunk c lies at
+        // c ^ (r & 7) of 128-byte rows, at c ^ (r / 2 & 3) of 64-byte rows
         if (a.out_t == DBF_F32) {
+          uint8_t* line = dst + lane * 128;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             *reinterpret_cast<uint4*>(line + ((j ^ (lane & 7)) << 4)) =
                 make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         } else {
+          uint8_t* line = dst + lane * 64;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 4; ++j) {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -587,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 w[e] = *reinterpret_cast<const uint32_t*>(&p2);
               }
             }
-            *reinterpret_cast<uint4*>(line + ((j ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(line + ((j ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
         if (a.tma_out) {
@@ -599,19 +575,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ++stores;
         } else {
+          // rows of y that do not start on 16 bytes: a lane per column, eight rows under way
           __syncwarp();
-          const int64_t left = a.q_rows - q0 - c0;
-          const int lim = static_cast<int>(min(static_cast<int64_t>(cols), left));
-          for (int r = 0; r < rows; ++r) {
-            const uint8_t* src = dst + r * 128;
-            for (int c = lane; c < lim; c += 32) {
-              if (a.out_t == DBF_F32) {
-                static_cast<uint32_t*>(a.out)[(row0 + r) * a.ld_out + q0 + c0 + c] =
-                    *reinterpret_cast<const uint32_t*>(src + (((c >> 2) ^ (r & 7)) << 4) + 4 * (c & 3));
-              } else {
-                static_cast<uint16_t*>(a.out)[(row0 + r) * a.ld_out + q0 + c0 + c] =
-                    *reinterpret_cast<const uint16_t*>(src + (((c >> 3) ^ (r & 7)) << 4) + 2 * (c & 7));
-              }
+          const bool in = q0 + c0 + lane < a.q_rows;
+          const int64_t at = row0 * a.ld_out + q0 + c0 + lane;
+          for (int r = 0; r < rows; r += 8) {
+            uint32_t e[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int rr = r + k;
+              e[k] = a.out_t == DBF_F32
+                         ? *reinterpret_cast<const uint32_t*>(dst + rr * 128 + (((lane >> 2) ^ (rr & 7)) << 4) + 4 * (lane & 3))
+                         : *reinterpret_cast<const uint16_t*>(dst + rr * 64 + (((lane >> 3) ^ ((rr >> 1) & 3)) << 4) +
+                                                              2 * (lane & 7));
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              if (!in || r + k >= rows) continue;
+              if (a.out_t == DBF_F32) static_cast<uint32_t*>(a.out)[at + (r + k) * a.ld_out] = e[k];
+              else static_cast<uint16_t*>(a.out)[at + (r + k) * a.ld_out] = static_cast<uint16_t>(e[k]);
             }
           }
           __syncwarp();
@@ -662,11 +644,11 @@ bool operand_map(const Operand& o, int64_t pitch, bool packed, int box_rows, CUt
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int KA, int NT, bool WROWS>
-dbf_status launch_gemm(const Operand& p, const Operand& q, MxArgs a, int64_t pitch, int ks, const DeviceInfo& dev,
-                       cudaStream_t stream) {
-  using C = Cfg<KA, NT, WROWS>;
-  auto kernel = dbf_mx_gemm_kernel<KA, NT, WROWS>;
+template <int KA, int NT>
+dbf_status launch_split(const Operand& p, const Operand& q, MxArgs a, int64_t pitch, int ks, const DeviceInfo& dev,
+                        cudaStream_t stream) {
+  using C = SplitCfg<KA, NT>;
+  auto kernel = dbf_mx_gemm_split_kernel<KA, NT>;
   static std::once_flag once[64];  // the attribute once per device
   static cudaError_t attr_err[64];
   std::call_once(once[dev.device], [&] {
@@ -716,19 +698,20 @@ bool scale_map(const Operand& o, int64_t k4s, int ka, int box_tiles, CUtensorMap
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The map of y for stores of 32 rows x 128 bytes.
+// The map of y for stores of 32 rows x 32 columns.
 bool out_map(void* y, int out_t, int64_t rows, int64_t cols, CUtensorMap* map) {
   auto encode = tensor_map_encoder();
   if (!encode) return false;
   const size_t e = dtype_size(out_t);
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * e};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / e), 32};
+  const cuuint32_t box[2] = {32, 32};
   const cuuint32_t estr[2] = {1, 1};
   const CUtensorMapDataType t = out_t == DBF_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                 : out_t == DBF_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  return encode(map, t, 2, y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return encode(map, t, 2, y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                e == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                 CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -747,7 +730,7 @@ dbf_status launch_pair(const Operand& x, const Operand& w, const MxArgs& m, int6
   a.p_rows = x.rows;
   a.q_rows = w.rows;
   a.k4s = m.k4s;
-  a.stages_k = m.stages_k;
+  a.steps_k = m.steps_k;
   const int p_tx = KA == 1 && x.four ? kRowBytes / 2 : kRowBytes, q_tx = KA == 1 && w.four ? kRowBytes / 2 : kRowBytes;
   a.tx = 2 * (kRows * p_tx + C::kQRows * q_tx + C::kScaleBytes);
   a.idesc = KA == 2 ? idesc_block_scaled(256, NT, 1, 1) : idesc_block_scaled(256, NT, x.four ? 5 : 0, w.four ? 5 : 0);
@@ -783,7 +766,7 @@ template <int KA>
 dbf_status launch_mx(const Operand& x, const Operand& w, const MxArgs& base, int64_t pitch, const DeviceInfo& dev,
                      cudaStream_t stream) {
   MxArgs a = base;
-  a.stages_k = static_cast<int>((a.k4s + KA - 1) / KA);
+  a.steps_k = static_cast<int>((a.k4s + KA - 1) / KA);
   // 256 tokens x 256 weight rows where those tiles occupy half the pairs; else the
   // weight's rows by the tokens, the K range split over up to eight CTAs
   const int64_t wide = (x.rows + 255) / 256 * ((w.rows + 255) / 256);
@@ -791,12 +774,12 @@ dbf_status launch_mx(const Operand& x, const Operand& w, const MxArgs& base, int
   const int nt = x.rows <= 16 ? 16 : x.rows <= 32 ? 32 : x.rows <= 64 ? 64 : 128;
   const int64_t tiles = (w.rows + kRows - 1) / kRows * ((x.rows + nt - 1) / nt);
   int ks = 1;
-  while (ks < 8 && tiles * ks * 2 <= dev.num_sms && ks * 2 <= a.stages_k) ks *= 2;
+  while (ks < 8 && tiles * ks * 2 <= dev.num_sms && ks * 2 <= a.steps_k) ks *= 2;
   switch (nt) {
-    case 16: return launch_gemm<KA, 16, true>(w, x, a, pitch, ks, dev, stream);
-    case 32: return launch_gemm<KA, 32, true>(w, x, a, pitch, ks, dev, stream);
-    case 64: return launch_gemm<KA, 64, true>(w, x, a, pitch, ks, dev, stream);
-    default: return launch_gemm<KA, 128, true>(w, x, a, pitch, ks, dev, stream);
+    case 16: return launch_split<KA, 16>(w, x, a, pitch, ks, dev, stream);
+    case 32: return launch_split<KA, 32>(w, x, a, pitch, ks, dev, stream);
+    case 64: return launch_split<KA, 64>(w, x, a, pitch, ks, dev, stream);
+    default: return launch_split<KA, 128>(w, x, a, pitch, ks, dev, stream);
   }
 }
 
@@ -836,7 +819,7 @@ dbf_status dbf_mx_forward(const uint8_t* x_codes, const uint8_t* x_scales, dbf_m
   if (st != DBF_OK) return st;
   MxArgs a{};
   a.k4s = mx_pitch(m_in) / 128;
-  a.p_static = (flags & DBF_FWD_WEIGHTS_STATIC) != 0;
+  a.w_static = (flags & DBF_FWD_WEIGHTS_STATIC) != 0;
   a.out = y;
   a.ld_out = n;
   a.out_t = y_t;
