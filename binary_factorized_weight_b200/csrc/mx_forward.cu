@@ -309,20 +309,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- many tiles: CTA pairs
-// Tiles of 256 tokens x NT weight rows, one per pair of CTAs (cta_group::2): each
-// CTA holds its 128 tokens and half of the tile's weight rows, so a stage costs
-// it 16 KB + NT/2 rows where a CTA alone would fetch NT; the MMA reads both.
-// The pairs are persistent (one CTA per SM) and walk the tiles, tokens fastest;
-// the ring runs on across tiles.  Accumulators: tensor memory holds two of NT
-// columns that overlap in their last / first columns where both do not fit
-// beside the scales, so the MMAs of a tile wait only until the epilogue has
-// read the shared columns of the tile before.
+// Tiles of 256 tokens x 256 weight rows, one per pair of CTAs (cta_group::2):
+// each CTA holds its 128 tokens and half of the tile's weight rows, so a step
+// costs it 32 KB where a CTA alone would fetch 48; the MMA reads both.  The
+// pairs are persistent (one CTA per SM) and walk the work items, tokens fastest;
+// the ring runs on across items.  Tiles that would leave most pairs idle (all of
+// few, or the last round's) are cut into 2 or 4 items of 128 or 64 weight rows.
+// Accumulators: tensor memory holds two of 256 columns that overlap in their
+// last / first columns (both do not fit beside the scales), so the MMAs of an
+// item wait only until the epilogue has read the shared columns of the one before.
 // The epilogue writes through shared memory with TMA stores (rows of y on 16
 // bytes), else row by row.
-template <int KA, int NT>
+constexpr int kPairCols = 256;  // weight rows of a whole tile
+template <int KA>
 struct PairCfg {
-  static constexpr int kQRows = NT / 2;
-  static constexpr int kQTiles = NT % 128 == 0 ? NT / 128 : (NT + 96 + 127) / 128;  // scale tiles a tile's rows touch
+  static constexpr int kQRows = kPairCols / 2;
+  static constexpr int kQTiles = kPairCols / 128;  // scale tiles of a tile's weight rows
   static constexpr int kPBytes = kRows * kRowBytes;
   static constexpr int kQBytes = kQRows * kRowBytes;
   static constexpr int kScaleBytes = KA * (1 + kQTiles) * kTileBytes;
@@ -331,21 +333,20 @@ struct PairCfg {
   static constexpr int kBufs = 3;            // per epilogue warp
   static constexpr int kEpiBytes = 4 * kBufs * kWarpBuf;
   static constexpr int kRoom = 227 * 1024 - 1024 - 512 - kEpiBytes;
-  static constexpr int kStages = kRoom / kStageBytes < 6 ? kRoom / kStageBytes : 6;
+  static constexpr int kMost = 5;  // more would cost the accumulators' columns
+  static constexpr int kStages = kRoom / kStageBytes < kMost ? kRoom / kStageBytes : kMost;
   static constexpr int kEpiOffset = kStages * (kPBytes + kQBytes);
   static constexpr int kScaleOffset = kEpiOffset + kEpiBytes;
   static constexpr int kBarOffset = kScaleOffset + kStages * kScaleBytes;
   static constexpr int kSmemBytes = kBarOffset + 512 + 1024;
   // scales in tensor memory: a copy may overtake the MMAs issued before it, so a
-  // stage's scales go where no running MMA reads
+  // stage's place is its own as long as its slot of the ring is
   static constexpr int kScaleCols = 4 * KA * (1 + kQTiles);
-  static constexpr int kScaleBufs = 512 - 2 * NT >= 2 * kScaleCols && 512 - 2 * NT < 3 * kScaleCols ? 2 : 3;
-  static constexpr int kScaleBase = 512 - kScaleBufs * kScaleCols;
-  static_assert(kStages > kScaleBufs, "a buffer's last stage must still be told from the next one in its place");
+  static constexpr int kScaleBase = 512 - kStages * kScaleCols;
   // the second accumulator starts where it still ends before the scales
-  static constexpr int kAcc1 = 2 * NT <= kScaleBase ? NT : (kScaleBase - NT) / 32 * 32;
-  static constexpr int kShared = NT - kAcc1;  // columns both accumulators use
-  static_assert(kShared % 32 == 0 && kShared <= 96, "");
+  static constexpr int kAcc1 = (kScaleBase - kPairCols) / 32 * 32;
+  static constexpr int kShared = kPairCols - kAcc1;  // columns both accumulators use
+  static_assert(kShared % 32 == 0 && kShared <= 128, "");
 };
 
 struct PairArgs {
@@ -353,7 +354,9 @@ struct PairArgs {
   int64_t k4s;
   int steps_k;
   int tx;  // bytes of a stage, both CTAs
-  uint32_t idesc;
+  uint32_t idesc;  // without N
+  int64_t whole;   // items that are whole tiles; the tiles behind them are cut
+  int cut;         // into this many items each (1, 2 or 4)
   void* out;
   int64_t ld_out;
   int out_t;
@@ -361,12 +364,12 @@ struct PairArgs {
   int* status;
 };
 
-template <int KA, int NT>
+template <int KA>
 __global__ void __launch_bounds__(kThreads, 1)
     dbf_mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap p_map, const __grid_constant__ CUtensorMap q_map,
                             const __grid_constant__ CUtensorMap ps_map, const __grid_constant__ CUtensorMap qs_map,
                             const __grid_constant__ CUtensorMap y_map, const PairArgs a) {
-  using C = PairCfg<KA, NT>;
+  using C = PairCfg<KA>;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -386,8 +389,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(cluster_rank());
   const int64_t p_tiles = (a.p_rows + 255) / 256;
-  const int64_t tiles = p_tiles * ((a.q_rows + NT - 1) / NT);
+  const int64_t tiles = p_tiles * ((a.q_rows + kPairCols - 1) / kPairCols);
+  const int64_t items = a.whole + (tiles - a.whole) * a.cut;
   const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  struct Item {
+    int64_t p0, q0;  // first token, first weight row
+    int cols;        // weight rows
+  };
+  auto item = [&](int64_t i) {
+    const int64_t j = i - a.whole;
+    const int64_t tile = j < 0 ? i : a.whole + j / a.cut;
+    const int cols = j < 0 ? kPairCols : kPairCols / a.cut;
+    return Item{(tile % p_tiles) * 256, (tile / p_tiles) * kPairCols + (j < 0 ? 0 : j % a.cut * cols), cols};
+  };
 
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
@@ -427,9 +441,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       uint32_t it = 0;
       pdl_wait();
-      for (int64_t t = pair; t < tiles && ok; t += pairs) {
-        const int p0 = static_cast<int>((t % p_tiles) * 256) + rank * kRows;
-        const int64_t q0 = (t / p_tiles) * NT;
+      for (int64_t t = pair; t < items && ok; t += pairs) {
+        const Item w = item(t);
+        const int p0 = static_cast<int>(w.p0) + rank * kRows, q0 = static_cast<int>(w.q0);
         for (int kt = 0; kt < a.steps_k; ++kt, ++it) {
           const int s = static_cast<int>(it % S);
           if (it >= S && !mbar_wait_often<true>(&empty[s], (it / S - 1) & 1, abort_flag, a.status)) {
@@ -440,9 +454,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t bar = map_to_rank(&full[s], 0);
           uint8_t* sc = s_st + s * C::kScaleBytes;
           tma_load_2d_pair(p_st + s * C::kPBytes, &p_map, kt * 128, p0, bar);
-          tma_load_2d_pair(q_st + s * C::kQBytes, &q_map, kt * 128, static_cast<int>(q0) + rank * C::kQRows, bar);
+          tma_load_2d_pair(q_st + s * C::kQBytes, &q_map, kt * 128, q0 + rank * (w.cols / 2), bar);
           tma_load_2d_pair(sc, &ps_map, kt * 128 * KA, p0 >> 7, bar);
-          tma_load_2d_pair(sc + KA * kTileBytes, &qs_map, kt * 128 * KA, static_cast<int>(q0 >> 7), bar);
+          tma_load_2d_pair(sc + KA * kTileBytes, &qs_map, kt * 128 * KA, q0 >> 7, bar);
         }
       }
       // after a wait that gave up: no copy may still be on its way when the CTAs end
@@ -457,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (rank == 0 && elect_one()) {
       bool ok = true;
       uint32_t it = 0, n = 0;
-      for (int64_t t = pair; t < tiles && ok; t += pairs, ++n) {
+      for (int64_t t = pair; t < items && ok; t += pairs, ++n) {
         const uint32_t b = n & 1, use = n >> 1;
         // this accumulator's last tile has been read, and the tile before has
         // left the shared columns
@@ -466,19 +480,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait_often<true>(&acc_shared[b ^ 1], ((n - 1) >> 1) & 1, abort_flag, a.status);
         if (!ok) break;
         const uint32_t d = tmem + b * C::kAcc1;
-        // where the tile's first weight row lies in its scale tile
-        const uint32_t q_col = static_cast<uint32_t>(((t / p_tiles) * NT & 127) >> 5);
+        const Item w = item(t);
+        // where the item's first weight row lies in its scale tile (column 0 or 2)
+        const uint32_t q_col = static_cast<uint32_t>(w.q0 & 127) >> 5;
+        const uint32_t idesc = a.idesc | (static_cast<uint32_t>(w.cols >> 3) << 17);
         for (int kt = 0; kt < a.steps_k; ++kt, ++it) {
           const int s = static_cast<int>(it % S);
           ok = mbar_wait_often<true>(&full[s], (it / S) & 1, abort_flag, a.status);
-          // the MMAs that read this stage's scale buffer before have completed
-          if (ok && it >= C::kScaleBufs) {
-            const uint32_t old = it - C::kScaleBufs;
-            ok = mbar_wait_often<true>(&empty[old % S], (old / S) & 1, abort_flag, a.status);
-          }
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sfa = tmem + C::kScaleBase + (it % C::kScaleBufs) * C::kScaleCols, sfb = sfa + 4 * KA;
+          const uint32_t sfa = tmem + C::kScaleBase + s * C::kScaleCols, sfb = sfa + 4 * KA;
           const uint32_t sc = smem_u32(s_st + s * C::kScaleBytes);
 #pragma unroll
           for (int k = 0; k < KA; ++k) {
@@ -494,11 +505,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t pd = smem_desc_sw128_kmajor(pa + kk * 32), qd = smem_desc_sw128_kmajor(qa + kk * 32);
             if constexpr (KA == 2) {
               const uint32_t id = 2u * (kk & 1);
-              tc_mma_mxf4_pair(d, pd, qd, a.idesc | (id << 4) | (id << 29), sfa + 4 * (kk >> 1),
+              tc_mma_mxf4_pair(d, pd, qd, idesc | (id << 4) | (id << 29), sfa + 4 * (kk >> 1),
                                sfb + q_col + 4 * C::kQTiles * (kk >> 1), acc);
             } else {
               tc_mma_mxf8f6f4_pair(d, pd, qd,
-                                   a.idesc | (static_cast<uint32_t>(kk) << 4) | (static_cast<uint32_t>(kk) << 29), sfa,
+                                   idesc | (static_cast<uint32_t>(kk) << 4) | (static_cast<uint32_t>(kk) << 29), sfa,
                                    sfb + q_col, acc);
             }
           }
@@ -513,28 +524,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3;  // the TMEM lanes this warp may read
     uint8_t* buf = epi_st + q * (C::kBufs * C::kWarpBuf);
     uint32_t n = 0, stores = 0;
-    for (int64_t t = pair; t < tiles; t += pairs, ++n) {
+    for (int64_t t = pair; t < items; t += pairs, ++n) {
       const uint32_t b = n & 1;
       if (!__all_sync(0xffffffffu, mbar_wait_often<true>(&acc_full[b], (n >> 1) & 1, abort_flag, a.status))) break;
       tc_fence_after();
       const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * C::kAcc1;
-      const int64_t row0 = (t % p_tiles) * 256 + rank * kRows + q * 32, q0 = (t / p_tiles) * NT;
+      const Item w = item(t);
+      const int64_t row0 = w.p0 + rank * kRows + q * 32, q0 = w.q0;
       const int rows = static_cast<int>(max(int64_t{0}, min(int64_t{32}, a.p_rows - row0)));
-      // 32 columns at a time; those shared with the other accumulator first:
-      // the last ones of accumulator 0, the first of accumulator 1
-      for (int i = 0; i < NT / 32; ++i) {
-        const int c0 = b == 0 && C::kShared > 0 ? NT - (i + 1) * 32 : i * 32;
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(acc + c0, v);
-        tmem_ld_wait();
-        if ((i + 1) * 32 == C::kShared || i + 1 == NT / 32) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if ((i + 1) * 32 == C::kShared) mbar_arrive_remote_release(map_to_rank(&acc_shared[b], 0));
-            if (i + 1 == NT / 32) mbar_arrive_remote_release(map_to_rank(&acc_empty[b], 0));
-          }
-        }
+      // 32 columns at a time; those shared with the other accumulator first, and
+      // into registers all at once, so that its MMAs can start: the last ones of
+      // accumulator 0, the first of accumulator 1
+      auto column = [&](int i) { return b == 0 && C::kShared > 0 ? kPairCols - (i + 1) * 32 : i * 32; };
+      auto signal = [&](uint64_t* bar) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote_release(map_to_rank(bar, 0));
+      };
+      auto write = [&](int c0, const uint32_t (&v)[32]) {
+        if (c0 >= w.cols) return;
         uint8_t* dst = buf + (stores % C::kBufs) * C::kWarpBuf;
         // the store that last used this buffer has read it
         if (lane == 0) bulk_wait_read<C::kBufs - 1>();
@@ -551,19 +559,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* line = dst + lane * 64;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            uint32_t w[4];
+            uint32_t h[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float lo = __uint_as_float(v[8 * j + 2 * e]), hi = __uint_as_float(v[8 * j + 2 * e + 1]);
               if (a.out_t == DBF_F16) {
                 const __half2 p2 = __floats2half2_rn(lo, hi);
-                w[e] = *reinterpret_cast<const uint32_t*>(&p2);
+                h[e] = *reinterpret_cast<const uint32_t*>(&p2);
               } else {
                 const __nv_bfloat162 p2 = __floats2bfloat162_rn(lo, hi);
-                w[e] = *reinterpret_cast<const uint32_t*>(&p2);
+                h[e] = *reinterpret_cast<const uint32_t*>(&p2);
               }
             }
-            *reinterpret_cast<uint4*>(line + ((j ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(line + ((j ^ ((lane >> 1) & 3)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
           }
         }
         if (a.tma_out) {
@@ -598,6 +606,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
+      };
+      constexpr int kFirst = C::kShared / 32;
+      if constexpr (kFirst > 0) {
+        uint32_t v[kFirst][32];
+#pragma unroll
+        for (int i = 0; i < kFirst; ++i) tmem_ld_32x32b_x32(acc + column(i), v[i]);
+        tmem_ld_wait();
+        signal(&acc_shared[b]);
+#pragma unroll
+        for (int i = 0; i < kFirst; ++i) write(column(i), v[i]);
+      }
+#pragma unroll 1
+      for (int i = kFirst; i < kPairCols / 32; ++i) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(acc + column(i), v);
+        tmem_ld_wait();
+        if (i + 1 == kPairCols / 32) signal(&acc_empty[b]);
+        write(column(i), v);
       }
     }
     if (lane == 0) bulk_wait_all<0>();
@@ -715,11 +741,11 @@ bool out_map(void* y, int out_t, int64_t rows, int64_t cols, CUtensorMap* map) {
                 CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int KA, int NT>
+template <int KA>
 dbf_status launch_pair(const Operand& x, const Operand& w, const MxArgs& m, int64_t pitch, const DeviceInfo& dev,
                        cudaStream_t stream) {
-  using C = PairCfg<KA, NT>;
-  auto kernel = dbf_mx_gemm_pair_kernel<KA, NT>;
+  using C = PairCfg<KA>;
+  auto kernel = dbf_mx_gemm_pair_kernel<KA>;
   static std::once_flag once[64];  // the attribute once per device
   static cudaError_t attr_err[64];
   std::call_once(once[dev.device], [&] {
@@ -733,7 +759,7 @@ dbf_status launch_pair(const Operand& x, const Operand& w, const MxArgs& m, int6
   a.steps_k = m.steps_k;
   const int p_tx = KA == 1 && x.four ? kRowBytes / 2 : kRowBytes, q_tx = KA == 1 && w.four ? kRowBytes / 2 : kRowBytes;
   a.tx = 2 * (kRows * p_tx + C::kQRows * q_tx + C::kScaleBytes);
-  a.idesc = KA == 2 ? idesc_block_scaled(256, NT, 1, 1) : idesc_block_scaled(256, NT, x.four ? 5 : 0, w.four ? 5 : 0);
+  a.idesc = KA == 2 ? idesc_block_scaled(256, 0, 1, 1) : idesc_block_scaled(256, 0, x.four ? 5 : 0, w.four ? 5 : 0);
   a.out = m.out;
   a.ld_out = m.ld_out;
   a.out_t = m.out_t;
@@ -744,9 +770,16 @@ dbf_status launch_pair(const Operand& x, const Operand& w, const MxArgs& m, int6
       !scale_map(x, m.k4s, KA, 1, &ps_map) || !scale_map(w, m.k4s, KA, C::kQTiles, &qs_map) ||
       (a.tma_out && !out_map(m.out, m.out_t, x.rows, w.rows, &y_map)))
     return DBF_ERR_CUDA;
-  const int64_t tiles = (x.rows + 255) / 256 * ((w.rows + NT - 1) / NT);
+  // The tiles of the last round (all of them where they fill no round) are cut
+  // into 2 or 4 items as long as every pair gets one at most: an item of 64
+  // weight rows takes about half the time of a whole tile.
+  const int64_t tiles = (x.rows + 255) / 256 * ((w.rows + kPairCols - 1) / kPairCols);
+  const int64_t pairs = dev.num_sms / 2, left = tiles % pairs;
+  a.cut = left * 4 <= pairs ? 4 : left * 2 <= pairs ? 2 : 1;
+  a.whole = tiles - left;
+  const int64_t items = a.whole + left * a.cut;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, dev.num_sms / 2)));
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(items, pairs)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
@@ -770,7 +803,7 @@ dbf_status launch_mx(const Operand& x, const Operand& w, const MxArgs& base, int
   // 256 tokens x 256 weight rows where those tiles occupy half the pairs; else the
   // weight's rows by the tokens, the K range split over up to eight CTAs
   const int64_t wide = (x.rows + 255) / 256 * ((w.rows + 255) / 256);
-  if (x.rows > 64 && 4 * wide >= dev.num_sms) return launch_pair<KA, 256>(x, w, a, pitch, dev, stream);
+  if (x.rows > 64 && 4 * wide >= dev.num_sms) return launch_pair<KA>(x, w, a, pitch, dev, stream);
   const int nt = x.rows <= 16 ? 16 : x.rows <= 32 ? 32 : x.rows <= 64 ? 64 : 128;
   const int64_t tiles = (w.rows + kRows - 1) / kRows * ((x.rows + nt - 1) / nt);
   int ks = 1;
