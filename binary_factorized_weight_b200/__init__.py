@@ -16,6 +16,8 @@ Build the library with ``python -m binary_factorized_weight_b200.build``.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from typing import Optional
 
@@ -526,68 +528,41 @@ def dbf_factorize(W: torch.Tensor, Omega: torch.Tensor, passes: int = 10, admm_s
 
 
 # ---------------------------------------------------------------- microscaled matrices and the norm
-_FLOAT_CODES = {torch.float16: DBF_F16, torch.float32: DBF_F32, torch.bfloat16: DBF_BF16}
+# Checks of the arguments and output tensors are made in C++ (csrc/binding.cpp).
+_BINDING = None
 
 
-def _float_code(dtype: torch.dtype) -> int:
-    code = _FLOAT_CODES.get(dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {dtype}: float16, bfloat16 or float32")
-    return code
+def _raise_status(func: str, status: int):
+    raise DBFError(func, status)
 
 
-def _raw_stream(stream, *tensors) -> int:
-    """The stream's handle, after a check that the tensors are contiguous and lie on the current device."""
-    device = torch.cuda.current_device() if tensors[0].is_cuda else -1
-    for t in tensors:
-        if t is not None and (t.get_device() != device or device < 0 or not t.is_contiguous()):
-            raise ValueError("tensors must be contiguous and on the current CUDA device")
+def _binding():
+    """_mx_binding.so (built in-tree), given the entry points of the loaded libdbf.so."""
+    global _BINDING
+    if _BINDING is None:
+        path = os.path.join(_HERE, "_mx_binding.so")
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is not built; run `python -m binary_factorized_weight_b200.build`")
+        lib = load_library()
+        spec = importlib.util.spec_from_loader("_mx_binding", importlib.machinery.ExtensionFileLoader("_mx_binding", path))
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.init(_raise_status, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.dbf_mx_quantize, lib.dbf_mx_dequantize, lib.dbf_mx_forward, lib.dbf_rmsnorm_forward,
+            lib.dbf_rmsnorm_mx_forward, lib.dbf_rmsnorm_backward, lib.dbf_mx_code_bytes, lib.dbf_mx_scale_bytes,
+            lib.dbf_mx_forward_workspace_bytes, lib.dbf_rmsnorm_backward_workspace_bytes)))
+        _BINDING = mod
+    return _BINDING
+
+
+def _on(stream, call, *args):
+    """call(*args) with `stream` as the current one: outputs and scratch made there belong to it."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
-    if stream.device.index != device:
+        return call(*args)
+    if stream.device.index != torch.cuda.current_device():
         raise ValueError("the stream belongs to another device")
-    return stream.cuda_stream
-
-
-def _new(stream, size, dtype, device) -> torch.Tensor:
-    """An uninitialised tensor that belongs to the stream the call runs on."""
-    if stream is None:
-        return torch.empty(size, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(size, dtype=dtype, device=device)
-
-
-def _check_out(t: torch.Tensor, name: str, dtype: torch.dtype, numel: int, exact: bool = True):
-    if t.dtype != dtype or (t.numel() != numel if exact else t.numel() < numel):
-        raise ValueError(f"{name} must be a {dtype} tensor of {numel} elements")
-
-
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _mx_buffers(rows, cols, fmt, codes, scales, stream, device):
-    n_codes, n_scales = dbf_mx_code_bytes(rows, cols, fmt), dbf_mx_scale_bytes(rows, cols)
-    if n_codes == 0:
-        raise ValueError("rows, cols or fmt outside the MX contract")
-    if codes is None:
-        codes = _new(stream, n_codes, torch.uint8, device)
-    else:
-        _check_out(codes, "codes", torch.uint8, n_codes, exact=False)
-    if scales is None:
-        scales = _new(stream, n_scales, torch.uint8, device)
-    else:
-        _check_out(scales, "scales", torch.uint8, n_scales, exact=False)
-    return codes, scales
-
-
-def _check_mx(codes, scales, rows, cols, fmt, name):
-    n_codes = dbf_mx_code_bytes(rows, cols, fmt)
-    if n_codes == 0:
-        raise ValueError(f"{name}: rows, cols or fmt outside the MX contract")
-    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or codes.numel() < n_codes or \
-            scales.numel() < dbf_mx_scale_bytes(rows, cols):
-        raise ValueError(f"{name}: codes and scales must be uint8 tensors of dbf_mx_code_bytes and dbf_mx_scale_bytes")
+        return call(*args)
 
 
 def dbf_mx_code_bytes(rows: int, cols: int, fmt: int) -> int:
@@ -602,31 +577,14 @@ def dbf_mx_quantize(src: torch.Tensor, fmt: int, transpose: bool = False, codes:
                     scales: Optional[torch.Tensor] = None, stream=None):
     """Quantise a rows x cols matrix (fp16, bf16 or fp32), or its transpose, into blocks of 32 with a power-of-two
     scale; fmt: DBF_MX_E2M1 (4 bits) or DBF_MX_E4M3 (8 bits).  Returns (codes, scales), uint8 CUDA tensors."""
-    if src.dim() != 2:
-        raise ValueError("src must be a 2-D tensor")
-    rows, cols = src.shape
-    code = _float_code(src.dtype)
-    raw = _raw_stream(stream, src, codes, scales)
-    codes, scales = _mx_buffers(*((cols, rows) if transpose else (rows, cols)), fmt, codes, scales, stream, src.device)
-    _check("dbf_mx_quantize", load_library().dbf_mx_quantize(
-        src.data_ptr(), code, rows, cols, fmt, DBF_MX_TRANSPOSE if transpose else 0, codes.data_ptr(),
-        scales.data_ptr(), raw))
-    return codes, scales
+    return _on(stream, (_BINDING or _binding()).quantize, src, fmt, transpose, codes, scales)
 
 
 def dbf_mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int, fmt: int,
                       dst: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.float32,
                       stream=None) -> torch.Tensor:
     """The values of an MX matrix, rows x cols."""
-    raw = _raw_stream(stream, codes, scales, dst)
-    _check_mx(codes, scales, rows, cols, fmt, "dbf_mx_dequantize")
-    if dst is None:
-        dst = _new(stream, (rows, cols), dtype, codes.device)
-    elif dst.numel() != rows * cols:
-        raise ValueError("dst must have rows * cols elements")
-    _check("dbf_mx_dequantize", load_library().dbf_mx_dequantize(
-        codes.data_ptr(), scales.data_ptr(), rows, cols, fmt, dst.data_ptr(), _float_code(dst.dtype), raw))
-    return dst
+    return _on(stream, (_BINDING or _binding()).dequantize, codes, scales, rows, cols, fmt, dst, dtype)
 
 
 def dbf_mx_forward_workspace_bytes(n: int, m_in: int, batch: int) -> int:
@@ -643,66 +601,22 @@ def dbf_mx_forward(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch
                    y: Optional[torch.Tensor] = None, y_dtype: torch.dtype = torch.float16,
                    workspace: Optional[torch.Tensor] = None, flags: int = 0, stream=None) -> torch.Tensor:
     """y = X W^T of two MX matrices, X batch x m_in and W n x m_in; returns y (batch x n)."""
-    raw = _raw_stream(stream, x_codes, x_scales, w_codes, w_scales, y, workspace)
-    _check_mx(x_codes, x_scales, batch, m_in, x_fmt, "x")
-    _check_mx(w_codes, w_scales, n, m_in, w_fmt, "w")
-    if y is None:
-        y = _new(stream, (batch, n), y_dtype, x_codes.device)
-    elif y.numel() != batch * n:
-        raise ValueError("y must have batch * n elements")
-    if workspace is None:
-        with torch.cuda.stream(stream):
-            workspace = dbf_mx_new_workspace(n, m_in, batch, device=x_codes.device)
-    _check("dbf_mx_forward", load_library().dbf_mx_forward(
-        x_codes.data_ptr(), x_scales.data_ptr(), x_fmt, w_codes.data_ptr(), w_scales.data_ptr(), w_fmt, n, m_in, batch,
-        y.data_ptr(), _float_code(y.dtype), workspace.data_ptr(), workspace.numel() * workspace.element_size(), flags,
-        raw))
-    return y
-
-
-def _norm_args(x, weight, residual, h, stream, *outs):
-    if x.dim() != 2:
-        raise ValueError("x must be a 2-D tensor")
-    rows, cols = x.shape
-    code = _float_code(x.dtype)
-    raw = _raw_stream(stream, x, weight, residual, h, *outs)
-    _check_out(weight, "weight", x.dtype, cols)
-    if residual is None:
-        if h is not None:
-            raise ValueError("h is written only with a residual")
-    else:
-        _check_out(residual, "residual", x.dtype, rows * cols)
-        if h is None:
-            h = _new(stream, (rows, cols), x.dtype, x.device)
-        else:
-            _check_out(h, "h", x.dtype, rows * cols)
-    return rows, cols, code, raw, h
+    return _on(stream, (_BINDING or _binding()).forward, x_codes, x_scales, w_codes, w_scales, n, m_in, batch, x_fmt,
+               w_fmt, y, y_dtype, workspace, flags)
 
 
 def dbf_rmsnorm_forward(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
                         h: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None, stream=None):
     """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight, per row of x (rows x cols; fp16, bf16 or fp32).
     Returns (y, h); h is x without a residual, and may be given as x or residual to be written in place."""
-    rows, cols, code, raw, h = _norm_args(x, weight, residual, h, stream, y)
-    if y is None:
-        y = _new(stream, (rows, cols), x.dtype, x.device)
-    else:
-        _check_out(y, "y", x.dtype, rows * cols)
-    _check("dbf_rmsnorm_forward", load_library().dbf_rmsnorm_forward(
-        x.data_ptr(), _addr(residual), weight.data_ptr(), code, rows, cols, eps, _addr(h), y.data_ptr(), raw))
-    return y, x if h is None else h
+    return _on(stream, (_BINDING or _binding()).norm, x, weight, eps, residual, h, y)
 
 
 def dbf_rmsnorm_mx_forward(x: torch.Tensor, weight: torch.Tensor, eps: float, fmt: int = DBF_MX_E4M3,
                            residual: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
                            codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None, stream=None):
     """dbf_rmsnorm_forward with y quantised as dbf_mx_quantize does; returns (codes, scales, h)."""
-    rows, cols, code, raw, h = _norm_args(x, weight, residual, h, stream, codes, scales)
-    codes, scales = _mx_buffers(rows, cols, fmt, codes, scales, stream, x.device)
-    _check("dbf_rmsnorm_mx_forward", load_library().dbf_rmsnorm_mx_forward(
-        x.data_ptr(), _addr(residual), weight.data_ptr(), code, rows, cols, eps, fmt, _addr(h), codes.data_ptr(),
-        scales.data_ptr(), raw))
-    return codes, scales, x if h is None else h
+    return _on(stream, (_BINDING or _binding()).norm_mx, x, weight, eps, fmt, residual, h, codes, scales)
 
 
 def dbf_rmsnorm_backward_workspace_bytes(rows: int, cols: int) -> int:
@@ -719,21 +633,4 @@ def dbf_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor
                          dweight: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
     """The norm's gradients: returns (dx, dweight), dx of dy's type (the gradient of x and of the residual, with dh,
     the gradient that reaches h by the residual stream, added) and dweight in fp32."""
-    rows, cols, code, raw, _ = _norm_args(h, weight, None, None, stream, dy, dh, dx, dweight, workspace)
-    _check_out(dy, "dy", h.dtype, rows * cols)
-    if dh is not None:
-        _check_out(dh, "dh", h.dtype, rows * cols)
-    if dx is None:
-        dx = _new(stream, (rows, cols), h.dtype, h.device)
-    else:
-        _check_out(dx, "dx", h.dtype, rows * cols)
-    if dweight is None:
-        dweight = _new(stream, (cols,), torch.float32, h.device)
-    else:
-        _check_out(dweight, "dweight", torch.float32, cols)
-    if workspace is None:
-        workspace = _new(stream, dbf_rmsnorm_backward_workspace_bytes(rows, cols), torch.uint8, h.device)
-    _check("dbf_rmsnorm_backward", load_library().dbf_rmsnorm_backward(
-        dy.data_ptr(), h.data_ptr(), weight.data_ptr(), _addr(dh), code, rows, cols, eps, dx.data_ptr(),
-        dweight.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw))
-    return dx, dweight
+    return _on(stream, (_BINDING or _binding()).norm_backward, dy, h, weight, eps, dh, dx, dweight, workspace)

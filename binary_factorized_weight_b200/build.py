@@ -4,7 +4,9 @@
 
 The shared library is written next to this file so that it travels with the
 repository; nothing is installed into site-packages.  Compilation is one nvcc
-call per .cu file (in parallel) followed by one link.
+call per .cu file (in parallel) followed by one link.  Beside it goes
+_mx_binding.so, the C++ part of the Python binding (csrc/binding.cpp), compiled
+with g++ against the installed torch's headers.
 """
 from __future__ import annotations
 
@@ -14,12 +16,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libdbf.so")
+BINDING = os.path.join(HERE, "_mx_binding.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["dbf_api.cu", "decode.cu", "fused.cu", "prefill.cu", "pack.cu", "transpose.cu", "reconstruct.cu", "bqq.cu", "factorize.cu", "noalloc.cu",
@@ -53,7 +57,41 @@ def _fingerprint() -> str:
     return h.hexdigest()
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compile _mx_binding.so for the torch that is installed."""
+    import torch
+
+    src = os.path.join(CSRC, "binding.cpp")
+    h = hashlib.sha256(f"{torch.__version__} {sys.version}".encode())
+    for name in (src, os.path.join(INCLUDE, "dbf.h")):
+        with open(name, "rb") as f:
+            h.update(f.read())
+    stamp, fp = BINDING + ".stamp", h.hexdigest()
+    if not force and os.path.exists(BINDING) and os.path.exists(stamp) and open(stamp).read() == fp:
+        return BINDING
+    from torch.utils import cpp_extension
+
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{p}" for p in cpp_extension.include_paths()], f"-I{sysconfig.get_paths()['include']}",
+           f"-I{os.path.join(cuda, 'include')}", src, "-o", tmp, f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{res.stdout}\n{res.stderr}")
+    if verbose:
+        sys.stderr.write(res.stdout + res.stderr)
+    os.replace(tmp, BINDING)
+    with open(stamp, "w") as f:
+        f.write(fp)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    build_binding(force=force, verbose=verbose)
     stamp = LIB + ".stamp"
     fp = _fingerprint()
     if not force and os.path.exists(LIB) and os.path.exists(stamp) and open(stamp).read() == fp:

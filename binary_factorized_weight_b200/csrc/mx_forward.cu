@@ -670,11 +670,21 @@ bool operand_map(const Operand& o, int64_t pitch, bool packed, int box_rows, CUt
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// CTAs of a cluster that share a tile's K range: as many as the SMs hold, up to
+// eight, with a step of K each at least.
+int split_ways(int64_t tiles, int steps, int num_sms) {
+  int ks = 1;
+  while (ks < 8 && tiles * ks * 2 <= num_sms && ks * 2 <= steps) ks *= 2;
+  return ks;
+}
+
 template <int KA, int NT>
-dbf_status launch_split(const Operand& p, const Operand& q, MxArgs a, int64_t pitch, int ks, const DeviceInfo& dev,
+dbf_status launch_split(const Operand& p, const Operand& q, MxArgs a, int64_t pitch, const DeviceInfo& dev,
                         cudaStream_t stream) {
   using C = SplitCfg<KA, NT>;
   auto kernel = dbf_mx_gemm_split_kernel<KA, NT>;
+  const int64_t tiles = (p.rows + kRows - 1) / kRows * ((q.rows + NT - 1) / NT);
+  int ks = split_ways(tiles, a.steps_k, dev.num_sms);
   static std::once_flag once[64];  // the attribute once per device
   static cudaError_t attr_err[64];
   std::call_once(once[dev.device], [&] {
@@ -692,10 +702,8 @@ dbf_status launch_split(const Operand& p, const Operand& q, MxArgs a, int64_t pi
   a.p_tx = KA == 1 && p.four ? kRowBytes / 2 : kRowBytes;
   a.q_tx = KA == 1 && q.four ? kRowBytes / 2 : kRowBytes;
   a.idesc = KA == 2 ? idesc_block_scaled(kRows, NT, 1, 1) : idesc_block_scaled(kRows, NT, p.four ? 5 : 0, q.four ? 5 : 0);
-  const int64_t tiles = (p.rows + kRows - 1) / kRows * ((q.rows + NT - 1) / NT);
   if (tiles * ks > 0x7fffffffLL) return DBF_ERR_UNSUPPORTED_SHAPE;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * ks));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
@@ -708,6 +716,26 @@ dbf_status launch_split(const Operand& p, const Operand& q, MxArgs a, int64_t pi
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  // No more clusters than the GPU holds at once (a GPC's SMs are no multiple of
+  // eight): a second round would double the time.  16 tiles of 4096: 12.5 us over
+  // eight CTAs each, 8.2 over four.
+  while (ks > 1) {
+    static std::once_flag asked[64][4];
+    static int most[64][4];
+    const int lg = ks == 2 ? 1 : ks == 4 ? 2 : 3;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(ks);
+    cfg.gridDim = dim3(static_cast<unsigned>(dev.num_sms / ks * ks));
+    std::call_once(asked[dev.device][lg], [&] {
+      if (cudaOccupancyMaxActiveClusters(&most[dev.device][lg], kernel, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        most[dev.device][lg] = 0;
+      }
+    });
+    if (tiles <= most[dev.device][lg]) break;
+    ks /= 2;
+  }
+  attr[1].val.clusterDim.x = static_cast<unsigned>(ks);
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * ks));
   return cudaLaunchKernelEx(&cfg, kernel, p_map, q_map, a) == cudaSuccess ? DBF_OK : DBF_ERR_CUDA;
 }
 
@@ -741,6 +769,18 @@ bool out_map(void* y, int out_t, int64_t rows, int64_t cols, CUtensorMap* map) {
                 CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The tiles of the last round (all of them where they fill no round) are cut
+// into 2 or 4 items as long as every pair gets one at most.
+struct PairPlan {
+  int64_t whole, left;  // whole tiles in full rounds, tiles of the last round
+  int cut;
+};
+PairPlan pair_plan(int64_t tokens, int64_t rows, int num_sms) {
+  const int64_t tiles = (tokens + 255) / 256 * ((rows + kPairCols - 1) / kPairCols);
+  const int64_t pairs = num_sms / 2, left = tiles % pairs;
+  return {tiles - left, left, left * 4 <= pairs ? 4 : left * 2 <= pairs ? 2 : 1};
+}
+
 template <int KA>
 dbf_status launch_pair(const Operand& x, const Operand& w, const MxArgs& m, int64_t pitch, const DeviceInfo& dev,
                        cudaStream_t stream) {
@@ -770,14 +810,10 @@ dbf_status launch_pair(const Operand& x, const Operand& w, const MxArgs& m, int6
       !scale_map(x, m.k4s, KA, 1, &ps_map) || !scale_map(w, m.k4s, KA, C::kQTiles, &qs_map) ||
       (a.tma_out && !out_map(m.out, m.out_t, x.rows, w.rows, &y_map)))
     return DBF_ERR_CUDA;
-  // The tiles of the last round (all of them where they fill no round) are cut
-  // into 2 or 4 items as long as every pair gets one at most: an item of 64
-  // weight rows takes about half the time of a whole tile.
-  const int64_t tiles = (x.rows + 255) / 256 * ((w.rows + kPairCols - 1) / kPairCols);
-  const int64_t pairs = dev.num_sms / 2, left = tiles % pairs;
-  a.cut = left * 4 <= pairs ? 4 : left * 2 <= pairs ? 2 : 1;
-  a.whole = tiles - left;
-  const int64_t items = a.whole + left * a.cut;
+  const PairPlan plan = pair_plan(x.rows, w.rows, dev.num_sms);
+  a.cut = plan.cut;
+  a.whole = plan.whole;
+  const int64_t items = plan.whole + plan.left * plan.cut, pairs = dev.num_sms / 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(items, pairs)));
   cfg.blockDim = dim3(kThreads);
@@ -800,20 +836,29 @@ dbf_status launch_mx(const Operand& x, const Operand& w, const MxArgs& base, int
                      cudaStream_t stream) {
   MxArgs a = base;
   a.steps_k = static_cast<int>((a.k4s + KA - 1) / KA);
-  // 256 tokens x 256 weight rows where those tiles occupy half the pairs; else the
-  // weight's rows by the tokens, the K range split over up to eight CTAs
-  const int64_t wide = (x.rows + 255) / 256 * ((w.rows + 255) / 256);
-  if (x.rows > 64 && 4 * wide >= dev.num_sms) return launch_pair<KA>(x, w, a, pitch, dev, stream);
-  const int nt = x.rows <= 16 ? 16 : x.rows <= 32 ? 32 : x.rows <= 64 ? 64 : 128;
-  const int64_t tiles = (w.rows + kRows - 1) / kRows * ((x.rows + nt - 1) / nt);
-  int ks = 1;
-  while (ks < 8 && tiles * ks * 2 <= dev.num_sms && ks * 2 <= a.steps_k) ks *= 2;
-  switch (nt) {
-    case 16: return launch_split<KA, 16>(w, x, a, pitch, ks, dev, stream);
-    case 32: return launch_split<KA, 32>(w, x, a, pitch, ks, dev, stream);
-    case 64: return launch_split<KA, 64>(w, x, a, pitch, ks, dev, stream);
-    default: return launch_split<KA, 128>(w, x, a, pitch, ks, dev, stream);
+  if (x.rows > 64) {
+    // Estimated microseconds of both kernels, from times measured at 1024 and
+    // 4096 x 4096, 14336 x 4096, 4096 x 14336 and 4096 x 512 for 32 to 2048
+    // tokens: a step of K costs a CTA of the split kernel 0.44 (4-bit operands,
+    // twice the K: 0.62), a pair 0.34 / 0.27 / 0.25 for 256 / 128 / 64 weight
+    // rows (4-bit: 0.39 / 0.32 / 0.30).
+    const bool four = KA == 2;
+    const int64_t split_tiles = (w.rows + kRows - 1) / kRows * ((x.rows + 127) / 128);
+    const int ks = split_ways(split_tiles, a.steps_k, dev.num_sms);
+    const double split_rounds = static_cast<double>((split_tiles * ks + dev.num_sms - 1) / dev.num_sms);
+    const double split_us = 3.5 + split_rounds * ((a.steps_k + ks - 1) / ks * (four ? 0.62 : 0.44) + 2.5);
+    const PairPlan plan = pair_plan(x.rows, w.rows, dev.num_sms);
+    const double cut_us = plan.left == 0 ? 0. : plan.cut == 1 ? (four ? 0.39 : 0.34) : plan.cut == 2 ? (four ? 0.32 : 0.27) : (four ? 0.30 : 0.25);
+    const double pair_us = 4.5 + a.steps_k * (static_cast<double>(plan.whole / (dev.num_sms / 2)) * (four ? 0.39 : 0.34) + cut_us);
+    // rows of y that do not start on 16 bytes cost the pairs' epilogue about 8 us a round
+    const bool aligned = a.ld_out * static_cast<int64_t>(dtype_size(a.out_t)) % 16 == 0;
+    const double store_us = aligned ? 0. : 8. * (static_cast<double>(plan.whole / (dev.num_sms / 2)) + (plan.left ? 1. / plan.cut : 0.));
+    if (pair_us + store_us < split_us) return launch_pair<KA>(x, w, a, pitch, dev, stream);
+    return launch_split<KA, 128>(w, x, a, pitch, dev, stream);
   }
+  if (x.rows <= 16) return launch_split<KA, 16>(w, x, a, pitch, dev, stream);
+  if (x.rows <= 32) return launch_split<KA, 32>(w, x, a, pitch, dev, stream);
+  return launch_split<KA, 64>(w, x, a, pitch, dev, stream);
 }
 
 constexpr int64_t kMaxReduce = int64_t{1} << 20;

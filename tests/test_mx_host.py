@@ -82,9 +82,9 @@ def test_norm_refusals(lib, change, status):
 @pytest.mark.parametrize("change,status", [
     (dict(dy=None), INVALID), (dict(h=None), INVALID), (dict(dx=None), INVALID), (dict(dw=None), INVALID),
     (dict(t=I8), INVALID), (dict(rows=0), INVALID), (dict(eps=0.0), INVALID), (dict(cols=(1 << 20) + 1), SHAPE),
-    (dict(dw=P + 2), MISALIGNED), (dict(dh=P + 1), MISALIGNED), (dict(work=None), WORKSPACE), (dict(wb=2 * 64 * 4 - 1), WORKSPACE)])
+    (dict(dw=P + 2), MISALIGNED), (dict(dh=P + 1), MISALIGNED), (dict(work=None), WORKSPACE), (dict(wb=64 * 4 - 1), WORKSPACE)])
 def test_norm_backward_refusals(lib, change, status):
-    a = dict(dy=P, h=P, w=P, dh=None, t=F16, rows=2, cols=64, eps=1e-5, dx=P, dw=P, work=P, wb=2 * 64 * 4) | change
+    a = dict(dy=P, h=P, w=P, dh=None, t=F16, rows=2, cols=64, eps=1e-5, dx=P, dw=P, work=P, wb=64 * 4) | change
     assert lib.dbf_rmsnorm_backward(a["dy"], a["h"], a["w"], a["dh"], a["t"], a["rows"], a["cols"], a["eps"], a["dx"],
                                     a["dw"], a["work"], a["wb"], None) == status
 
