@@ -119,10 +119,21 @@ __global__ void __launch_bounds__(kTThreads<T>) dbf_mx_quantize_t_kernel(const T
         *reinterpret_cast<uint4*>(&tile[rr * kCols + (rr >> 5) * kPad + cc]) = v;
       }
     } else {
-      for (int i = tid; i < kTRows * kCols; i += kTThreads<T>) {
-        const int rr = i / kCols, cc = i % kCols;
-        const int64_t r = k4 * kTRows + rr, c = c0 + cc;
-        tile[rr * kCols + (rr >> 5) * kPad + cc] = r < rows && c < cols ? src[r * cols + c] : from_f32<T>(0.f);
+      // sixteen loads under way together
+#pragma unroll 1
+      for (int i0 = tid; i0 < kTRows * kCols; i0 += 16 * kTThreads<T>) {
+        T v[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int i = i0 + k * kTThreads<T>;
+          const int64_t r = k4 * kTRows + i / kCols, c = c0 + i % kCols;
+          v[k] = r < rows && c < cols ? src[r * cols + c] : from_f32<T>(0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int i = i0 + k * kTThreads<T>, rr = i / kCols;
+          tile[rr * kCols + (rr >> 5) * kPad + i % kCols] = v[k];
+        }
       }
     }
     __syncthreads();
