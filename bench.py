@@ -909,6 +909,71 @@ def run_factorize(args):
                                     "gemm_tflops": fl / (ms * 1e-3) / 1e12, "relative_errors": errors}}))
 
 
+def run_mx(args):
+    """The decoder-layer set as 4-bit microscaled layers: for each distinct shape the
+    weight's quantisation, and at batch 1, 16, 128 and 2048 the norm that quantises its
+    input to 8 bits and the product, each captured with four weights in turn (inputs beyond
+    L2 together for the wide layers) and timed with CUDA events; the product's error
+    against the dense fp32 layer, and the norm's gradients at 2048 tokens."""
+    import torch
+
+    torch.cuda.set_device(0)
+    from binary_factorized_weight_b200 import build as lib_build
+
+    lib_build.build()
+    import binary_factorized_weight_b200 as dbf
+
+    gpu = torch.Generator(device="cuda")
+    gpu.manual_seed(4)
+
+    def timed(calls):
+        for call in calls:
+            call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(5):
+                for call in calls:
+                    call()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        us = []
+        for _ in range(8):
+            e0.record()
+            graph.replay()
+            e1.record()
+            torch.cuda.synchronize()
+            us.append(e0.elapsed_time(e1) * 1e3 / (5 * len(calls)))
+        return statistics.median(us[3:])
+
+    rows = []
+    for n, m_in in sorted({(s.n, s.m_in) for s in gen.LAYER_SET[1]}):
+        W = [(torch.randn(n, m_in, generator=gpu, device="cuda") * 0.02).to(torch.bfloat16) for _ in range(4)]
+        held = [dbf.dbf_mx_quantize(w, dbf.DBF_MX_E2M1) for w in W]
+        row = {"n": n, "m_in": m_in,
+               "quantize_us": timed([lambda w=w, h=h: dbf.dbf_mx_quantize(w, dbf.DBF_MX_E2M1, codes=h[0], scales=h[1])
+                                     for w, h in zip(W, held)])}
+        g = torch.ones(m_in, dtype=torch.bfloat16, device="cuda")
+        for batch in (1, 16, 128, 2048):
+            x = torch.randn(batch, m_in, generator=gpu, device="cuda").to(torch.bfloat16)
+            r = torch.randn(batch, m_in, generator=gpu, device="cuda").to(torch.bfloat16)
+            codes, scales, h = dbf.dbf_rmsnorm_mx_forward(x, g, 1e-5, residual=r)
+            ws = dbf.dbf_mx_new_workspace(n, m_in, batch)
+            y = torch.empty(batch, n, dtype=torch.bfloat16, device="cuda")
+            norm = lambda: dbf.dbf_rmsnorm_mx_forward(x, g, 1e-5, residual=r, h=h, codes=codes, scales=scales)  # noqa: E731
+            product = lambda q: dbf.dbf_mx_forward(codes, scales, *q, n, m_in, batch, y=y, workspace=ws,  # noqa: E731
+                                                   flags=dbf.DBF_FWD_WEIGHTS_STATIC)
+            row[f"norm_us_b{batch}"] = timed([norm])
+            row[f"product_us_b{batch}"] = timed([lambda q=q: product(q) for q in held])
+            dense = dbf.dbf_rmsnorm_forward(h, g, 1e-5)[0].float() @ W[0].float().t()
+            row[f"rel_error_b{batch}"] = float(((product(held[0]).float() - dense).norm() / dense.norm()).item())
+        dy, bws = torch.randn_like(h), dbf.dbf_rmsnorm_backward_new_workspace(2048, m_in)
+        dx, dw = torch.empty_like(h), torch.empty(m_in, dtype=torch.float32, device="cuda")
+        row["norm_backward_us_b2048"] = timed([lambda: dbf.dbf_rmsnorm_backward(dy, h, g, 1e-5, dh=dy, dx=dx, dweight=dw,
+                                                                                 workspace=bws)])
+        rows.append(row)
+    print(json.dumps({"mx": rows}))
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -928,6 +993,7 @@ def main():
                     help="only run this many dbf_forward calls of one layer (for ncu captures)")
     ap.add_argument("--flags", type=int, default=1, help="dbf_forward flags for --profile-calls (default: weights static)")
     ap.add_argument("--factorize", action="store_true", help="time the offline factorisation of a 4096^2 weight")
+    ap.add_argument("--mx", action="store_true", help="time the decoder-layer set as 4-bit microscaled layers")
     ap.add_argument("--fact-k", type=int, default=2048)
     ap.add_argument("--fact-passes", type=int, default=3)
     args = ap.parse_args()
@@ -936,6 +1002,8 @@ def main():
     shape = gen.CONFIGS[args.workload] if args.workload in gen.CONFIGS else layer_set[args.workload]
     if args.factorize:
         run_factorize(args)
+    elif args.mx:
+        run_mx(args)
     elif args.profile_calls > 0:
         run_profile_calls(args, shape, args.batch)
     elif args.sweep:

@@ -155,6 +155,7 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 5, [&] {
     const at::Tensor src = tensor(a[0]);
     const int fmt = format(a[1]), transpose = PyObject_IsTrue(a[2]);
+    if (transpose < 0) throw Refused{};
     OptTensor codes = optional_tensor(a[3]), scales = optional_tensor(a[4]);
     if (src.dim() != 2) refuse(PyExc_ValueError, "src must be a 2-D tensor");
     const dbf_dtype t = code_of(src.scalar_type());

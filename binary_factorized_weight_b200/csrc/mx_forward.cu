@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------ scale copies and MMAs
     if (elect_one()) {
+      pdl_wait();  // (the bounded waits start only when the kernel before has ended)
       bool ok = true;
       for (int it = 0; it < stages; ++it) {
         const int k = k0 + it * U, s = it % S;
@@ -234,6 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------ epilogue
+    pdl_wait();
     const int q = warp & 3;  // the TMEM lanes this warp may read
     const bool ok = __all_sync(0xffffffffu, mbar_wait_often<false>(acc_full, 0, abort_flag, a.status));
     tc_fence_after();
@@ -459,16 +461,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_2d_pair(sc + KA * kTileBytes, &qs_map, kt * 128 * KA, q0 >> 7, bar);
         }
       }
-      // after a wait that gave up: no copy may still be on its way when the CTAs end
-      if (*abort_flag && rank == 0) {
+      // after a wait that gave up: no copy may still be on its way when the CTAs
+      // end.  The even CTA's barriers count both CTAs' bytes; the odd one gives its
+      // copies, which take microseconds, a millisecond.
+      if (*abort_flag) {
         int never = 0;
-        for (uint32_t i = it < S ? 0 : it - S; i < it; ++i)
-          (void)mbar_wait_often<true>(&full[i % S], (i / S) & 1, &never, a.status);
+        if (rank == 0) {
+          for (uint32_t i = it < S ? 0 : it - S; i < it; ++i)
+            (void)mbar_wait_often<true>(&full[i % S], (i / S) & 1, &never, a.status);
+        } else {
+          const unsigned long long t0 = globaltimer_ns();
+          while (globaltimer_ns() - t0 < 1000000ull) {
+          }
+        }
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------ scale copies and MMAs (the even CTA's, for both)
     if (rank == 0 && elect_one()) {
+      pdl_wait();  // (the bounded waits start only when the kernel before has ended)
       bool ok = true;
       uint32_t it = 0, n = 0;
       for (int64_t t = pair; t < items && ok; t += pairs, ++n) {
@@ -521,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ------------------------------------------------ epilogue
+    pdl_wait();
     const int q = warp & 3;  // the TMEM lanes this warp may read
     uint8_t* buf = epi_st + q * (C::kBufs * C::kWarpBuf);
     uint32_t n = 0, stores = 0;
