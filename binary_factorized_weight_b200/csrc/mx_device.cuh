@@ -306,8 +306,8 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
 }
 
 // A warp's 512 neighbouring columns of one row -> codes and scales: the lane of
-// chunk c holds columns 16 c .., a block is two neighbouring lanes, a scale word
-// eight.  Nothing is written from pitch on (pitch: the padded row length, a
+// chunk c holds columns 16 c .., a block is two neighbouring lanes (the even one
+// stores its scale byte).  Nothing is written from pitch on (pitch: the padded row length, a
 // multiple of 128).
 template <int FMT>
 __device__ __forceinline__ void mx_store_row16(const float (&v)[kChunk], int64_t r, int64_t c, int64_t pitch,
@@ -322,10 +322,6 @@ __device__ __forceinline__ void mx_store_row16(const float (&v)[kChunk], int64_t
   uint32_t amax = __float_as_uint(m) & 0x7FFFFFFFu;
   amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   const uint32_t byte = mx_scale_byte<FMT>(amax);
-  const int lane = threadIdx.x & 31;
-  uint32_t word = byte << (8 * ((lane >> 1) & 3));
-  word |= __shfl_xor_sync(0xffffffffu, word, 2);
-  word |= __shfl_xor_sync(0xffffffffu, word, 4);
   if (kChunk * c >= pitch) return;
   const bool bad = byte == 255;
   const float inv = mx_inverse_scale(min(byte, 253u));
@@ -345,7 +341,7 @@ __device__ __forceinline__ void mx_store_row16(const float (&v)[kChunk], int64_t
                                mx_encode_e4m3(u[8], u[9], u[10], u[11]), mx_encode_e4m3(u[12], u[13], u[14], u[15]));
     *reinterpret_cast<uint4*>(codes + r * pitch + 16 * c) = bad ? make_uint4(0u, 0u, 0u, 0u) : q;
   }
-  if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(scales + mx_scale_word(r, c >> 3, pitch >> 7)) = word;
+  if ((c & 1) == 0) scales[mx_scale_word(r, c >> 3, pitch >> 7) + ((c >> 1) & 3)] = static_cast<uint8_t>(byte);
 }
 
 }  // namespace dbf

@@ -14,34 +14,39 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// it / n for the items of one launch: in 32 bits where they fit (a 64-bit
-// division costs as much as the rest of an item).
-__device__ __forceinline__ int64_t row_of(int64_t it, uint32_t n, bool small) {
-  return small ? static_cast<int64_t>(static_cast<uint32_t>(it) / n) : it / n;
+// How a block's warps share out rows: 2^lg warps to a row, each with 512
+// neighbouring columns at a time (sixteen per lane), so that no item needs a
+// division to find its row.
+struct Share {
+  int64_t row, row_step;  // this warp's first row, and the distance to its next
+  int group, group_step;  // its first group of 512 columns of a row, and the distance to the next
+};
+__device__ __forceinline__ Share share_of(int lg) {
+  const int warp = threadIdx.x >> 5;
+  const int rows = (kThreads / 32) >> lg;  // of a block
+  return {static_cast<int64_t>(blockIdx.x) * rows + (warp >> lg), static_cast<int64_t>(gridDim.x) * rows,
+          warp & ((1 << lg) - 1), 1 << lg};
 }
 
-// One warp item: 512 neighbouring columns of one row, sixteen per lane (32
-// bytes of 16-bit elements in one access).
 template <typename T, int FMT, bool VEC>
 __global__ void __launch_bounds__(kThreads) dbf_mx_quantize_kernel(const T* __restrict__ src, int64_t rows,
-                                                                   int64_t cols, int64_t pitch,
+                                                                   int64_t cols, int64_t pitch, int lg,
                                                                    uint8_t* __restrict__ codes,
                                                                    uint8_t* __restrict__ scales) {
   __shared__ alignas(32) T stage[VEC ? 1 : kThreads * kChunk];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t per_row = static_cast<uint32_t>((pitch + 511) >> 9);
-  const int64_t items = rows * per_row;
-  const bool small = items <= 0xffffffffll;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + warp; it < items; it += step) {
-    const int64_t r = row_of(it, per_row, small);
-    const int64_t c = (it - r * per_row) * 32 + lane;
-    const Pack16<T> p = load16<VEC>(src + r * cols, c, cols, stage + (VEC ? 0 : warp * 32 * kChunk));
-    float v[kChunk];
-    unpack16(p, v);
-    mx_store_row16<FMT>(v, r, c, pitch, codes, scales);
+  const int groups = static_cast<int>((pitch + 511) >> 9);
+  const Share w = share_of(lg);
+  for (int64_t r = w.row; r < rows; r += w.row_step) {
+    for (int g = w.group; g < groups; g += w.group_step) {
+      const int c = g * 32 + lane;
+      const Pack16<T> p = load16<VEC>(src + r * cols, c, cols, stage + (VEC ? 0 : warp * 32 * kChunk));
+      float v[kChunk];
+      unpack16(p, v);
+      mx_store_row16<FMT>(v, r, c, pitch, codes, scales);
+    }
   }
 }
 
@@ -153,42 +158,68 @@ __global__ void __launch_bounds__(kTThreads<T>) dbf_mx_quantize_t_kernel(const T
   }
 }
 
+// kUnroll rows of a warp are under way together: a row's codes are few bytes.
+constexpr int kUnroll = 2;
 template <typename T, int FMT, bool VEC>
 __global__ void __launch_bounds__(kThreads) dbf_mx_dequantize_kernel(const uint8_t* __restrict__ codes,
                                                                      const uint8_t* __restrict__ scales, int64_t rows,
-                                                                     int64_t cols, int64_t pitch, T* __restrict__ dst) {
+                                                                     int64_t cols, int64_t pitch, int lg,
+                                                                     T* __restrict__ dst) {
   __shared__ alignas(32) T stage[VEC ? 1 : kThreads * kChunk];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t per_row = static_cast<uint32_t>((cols + 511) >> 9);
-  const int64_t items = rows * per_row;
-  const bool small = items <= 0xffffffffll;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + warp; it < items; it += step) {
-    const int64_t r = row_of(it, per_row, small);
-    const int64_t c = (it - r * per_row) * 32 + lane;
-    Pack16<T> p;
-    if (kChunk * c < cols) {
-      float v[kChunk];
-      float(&lo)[8] = *reinterpret_cast<float(*)[8]>(&v[0]);
-      float(&hi)[8] = *reinterpret_cast<float(*)[8]>(&v[8]);
-      if constexpr (FMT == kMx4) {
-        const uint2 w = *reinterpret_cast<const uint2*>(codes + (r * pitch >> 1) + 8 * c);
-        mx_decode_e2m1(w.x, lo);
-        mx_decode_e2m1(w.y, hi);
-      } else {
-        const uint4 w = *reinterpret_cast<const uint4*>(codes + r * pitch + 16 * c);
-        mx_decode_e4m3(make_uint2(w.x, w.y), lo);
-        mx_decode_e4m3(make_uint2(w.z, w.w), hi);
-      }
-      const float s = mx_scale(scales[mx_scale_word(r, c >> 3, pitch >> 7) + ((c >> 1) & 3)]);
+  const int groups = static_cast<int>((cols + 511) >> 9);
+  const Share w = share_of(lg);
+  for (int64_t r0 = w.row; r0 < rows; r0 += kUnroll * w.row_step) {
+    for (int g = w.group; g < groups; g += w.group_step) {
+      const int c = g * 32 + lane;
+      uint32_t q[kUnroll][FMT == kMx4 ? 2 : 4];
+      uint32_t byte[kUnroll];
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) v[j] *= s;
-      p = pack16<T>(v);
+      for (int u = 0; u < kUnroll; ++u) {
+        const int64_t r = r0 + u * w.row_step;
+        if (r >= rows || kChunk * static_cast<int64_t>(c) >= cols) continue;
+        if constexpr (FMT == kMx4) {
+          *reinterpret_cast<uint2*>(q[u]) = *reinterpret_cast<const uint2*>(codes + (r * pitch >> 1) + 8 * static_cast<int64_t>(c));
+        } else {
+          *reinterpret_cast<uint4*>(q[u]) = *reinterpret_cast<const uint4*>(codes + r * pitch + 16 * static_cast<int64_t>(c));
+        }
+        byte[u] = scales[mx_scale_word(r, c >> 3, pitch >> 7) + ((c >> 1) & 3)];
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int64_t r = r0 + u * w.row_step;
+        if (r >= rows) break;
+        Pack16<T> p;
+        if (kChunk * static_cast<int64_t>(c) < cols) {
+          float v[kChunk];
+          float(&lo)[8] = *reinterpret_cast<float(*)[8]>(&v[0]);
+          float(&hi)[8] = *reinterpret_cast<float(*)[8]>(&v[8]);
+          if constexpr (FMT == kMx4) {
+            mx_decode_e2m1(q[u][0], lo);
+            mx_decode_e2m1(q[u][1], hi);
+          } else {
+            mx_decode_e4m3(make_uint2(q[u][0], q[u][1]), lo);
+            mx_decode_e4m3(make_uint2(q[u][2], q[u][3]), hi);
+          }
+          const float s = mx_scale(byte[u]);
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j) v[j] *= s;
+          p = pack16<T>(v);
+        }
+        store16<VEC>(dst + r * cols, c, cols, p, stage + (VEC ? 0 : warp * 32 * kChunk));
+      }
     }
-    store16<VEC>(dst + r * cols, c, cols, p, stage + (VEC ? 0 : warp * 32 * kChunk));
   }
+}
+
+// Warps to a row (as a power of two) for so many groups of 512 columns, and the
+// blocks that cover `rows`, `per` of them at a time in a warp.
+int warps_lg(int64_t groups) { return groups <= 1 ? 0 : groups <= 2 ? 1 : groups <= 4 ? 2 : 3; }
+unsigned row_blocks(int64_t rows, int lg, int per, const DeviceInfo& dev) {
+  const int64_t of_block = static_cast<int64_t>(per) * ((kThreads / 32) >> lg);
+  return static_cast<unsigned>(std::min<int64_t>((rows + of_block - 1) / of_block, int64_t{dev.num_sms} * 8));
 }
 
 unsigned grid_for(int64_t items, int64_t per_block, const DeviceInfo& dev) {
@@ -210,12 +241,12 @@ dbf_status quantize_typed(const void* src, int64_t rows, int64_t cols, bool tran
                             scales);
   }
   const int64_t pitch = mx_pitch(cols);
-  const int64_t items = rows * ((pitch + 511) >> 9);
+  const int lg = warps_lg((pitch + 511) >> 9);
   const bool vec = cols % kChunk == 0 && aligned_to(src, 32);
-  const dim3 grid(grid_for(items, kThreads / 32, dev));
-  return vec ? launch_pdl(dbf_mx_quantize_kernel<T, FMT, true>, grid, dim3(kThreads), 0, stream, s, rows, cols, pitch,
+  const dim3 grid(row_blocks(rows, lg, 1, dev));
+  return vec ? launch_pdl(dbf_mx_quantize_kernel<T, FMT, true>, grid, dim3(kThreads), 0, stream, s, rows, cols, pitch, lg,
                           codes, scales)
-             : launch_pdl(dbf_mx_quantize_kernel<T, FMT, false>, grid, dim3(kThreads), 0, stream, s, rows, cols, pitch,
+             : launch_pdl(dbf_mx_quantize_kernel<T, FMT, false>, grid, dim3(kThreads), 0, stream, s, rows, cols, pitch, lg,
                           codes, scales);
 }
 
@@ -224,13 +255,13 @@ dbf_status dequantize_typed(const uint8_t* codes, const uint8_t* scales, int64_t
                             const DeviceInfo& dev, cudaStream_t stream) {
   T* d = static_cast<T*>(dst);
   const int64_t pitch = mx_pitch(cols);
-  const int64_t items = rows * ((cols + 511) >> 9);
-  const dim3 grid(grid_for(items, kThreads / 32, dev));
+  const int lg = warps_lg((cols + 511) >> 9);
+  const dim3 grid(row_blocks(rows, lg, kUnroll, dev));
   const bool vec = cols % kChunk == 0 && aligned_to(dst, 32);
   return vec ? launch_pdl(dbf_mx_dequantize_kernel<T, FMT, true>, grid, dim3(kThreads), 0, stream, codes, scales, rows,
-                          cols, pitch, d)
+                          cols, pitch, lg, d)
              : launch_pdl(dbf_mx_dequantize_kernel<T, FMT, false>, grid, dim3(kThreads), 0, stream, codes, scales, rows,
-                          cols, pitch, d);
+                          cols, pitch, lg, d);
 }
 
 }  // namespace
