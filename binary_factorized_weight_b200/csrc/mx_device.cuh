@@ -260,9 +260,10 @@ __device__ __forceinline__ Pack16<T> load16(const T* row, int64_t c, int64_t col
   } else {
     const int lane = threadIdx.x & 31;
     const int64_t first = kChunk * (c - lane) + lane;
+    const int left = static_cast<int>(min(cols - first, int64_t{32 * kChunk}));
     T v[kChunk];
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j) v[j] = first + 32 * j < cols ? row[first + 32 * j] : from_f32<T>(0.f);
+    for (int j = 0; j < kChunk; ++j) v[j] = 32 * j < left ? row[first + 32 * j] : from_f32<T>(0.f);
     __syncwarp();  // earlier readers of the stage
 #pragma unroll
     for (int j = 0; j < kChunk; ++j) stage[32 * j + lane] = v[j];
@@ -292,9 +293,10 @@ __device__ __forceinline__ void store16(T* row, int64_t c, int64_t cols, const P
     for (int j = 0; j < static_cast<int>(sizeof(p) / 16); ++j) dst[j] = src[j];
     __syncwarp();
     const int64_t first = kChunk * (c - lane) + lane;
+    const int left = static_cast<int>(min(cols - first, int64_t{32 * kChunk}));
 #pragma unroll
     for (int j = 0; j < kChunk; ++j)
-      if (first + 32 * j < cols) row[first + 32 * j] = stage[32 * j + lane];
+      if (32 * j < left) row[first + 32 * j] = stage[32 * j + lane];
   }
 }
 

@@ -229,16 +229,15 @@ __device__ __forceinline__ void row_sums(float (&v)[M], float* red) {
 // distributed shared memory); sixteen columns per thread, whose sums of dweight
 // over the rows stay in registers and go to the row of `part`.
 // VEC: a thread owns sixteen neighbouring columns (32-byte accesses); else every
-// threads-th column.  PRE: the next row is loaded while this one is reduced (16-
+// 32nd of its warp's 512 columns.  PRE: the next row is loaded while this one is reduced (16-
 // bit elements: more does not fit the registers).
 constexpr int kGradThreads = 512;
 template <typename T, bool VEC, int SPAN>
 __global__ void __launch_bounds__(SPAN == 0 ? 32 * kWarpRows : kGradThreads, SPAN == 0 ? 2 : 1)
     dbf_rmsnorm_grad_kernel(const NormGradArgs p) {
-  constexpr int NV = 1, N = kChunk;
   constexpr bool PRE = sizeof(T) == 2, WARP = SPAN == 0;
   __shared__ float red[2][64];
-  __shared__ float sums[WARP ? kWarpRows * N * 32 : 1];
+  __shared__ float sums[WARP ? kWarpRows * kChunk * 32 : 1];
   __shared__ float2 ranks[SPAN == 2 ? 2 : 1][8];  // the cluster's sums of a row
   pdl_wait();
   pdl_launch_dependents();
@@ -248,59 +247,52 @@ __global__ void __launch_bounds__(SPAN == 0 ? 32 * kWarpRows : kGradThreads, SPA
     cluster_arrive_relaxed();
     cluster_wait_acquire();
   }
-  const int me = WARP ? threadIdx.x & 31 : rank * blockDim.x + threadIdx.x, threads = WARP ? 32 : ks * blockDim.x;
+  const int me = WARP ? threadIdx.x & 31 : rank * blockDim.x + threadIdx.x;
   const int group = WARP ? threadIdx.x >> 5 : 0;
   const int block = blockIdx.x / ks, blocks = gridDim.x / ks;  // a cluster counts as one
   const int64_t row0 = static_cast<int64_t>(block) * (WARP ? kWarpRows : 1) + group;
   const int64_t row_step = static_cast<int64_t>(blocks) * (WARP ? kWarpRows : 1);
-  // column of this thread's element n
-  auto column = [&](int n) -> int64_t {
-    return VEC ? kChunk * (me + static_cast<int64_t>(n / kChunk) * threads) + n % kChunk
-               : me + static_cast<int64_t>(n) * threads;
-  };
+  // this thread's first column, the distance between its columns, and how far the row goes from there
+  const int first = VEC ? kChunk * me : kChunk * (me & ~31) + (me & 31);
+  constexpr int kStride = VEC ? 1 : 32;
+  const int left = static_cast<int>(min(p.cols - first, int64_t{kStride * kChunk}));
   // this thread's elements of a row (zero behind the last column)
-  auto load = [&](const void* base, int64_t r, Pack16<T> (&a)[NV]) {
+  auto load = [&](const void* base, int64_t r) {
     const T* row = static_cast<const T*>(base) + r * p.cols;
+    if constexpr (VEC) {
+      return load16<true>(row, me, p.cols, static_cast<T*>(nullptr));
+    } else {
+      Pack16<T> a;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if constexpr (VEC) {
-        a[i] = load16<true>(row, me + static_cast<int64_t>(i) * threads, p.cols, static_cast<T*>(nullptr));
-      } else {
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) {
-          const int64_t c = column(kChunk * i + j);
-          a[i].e[j] = c < p.cols ? row[c] : from_f32<T>(0.f);
-        }
-      }
+      for (int j = 0; j < kChunk; ++j) a.e[j] = kStride * j < left ? row[first + kStride * j] : from_f32<T>(0.f);
+      return a;
     }
   };
   struct Row {
-    Pack16<T> h[NV], dy[NV], dh[NV];
+    Pack16<T> h, dy, dh;
   };
   auto load_row = [&](int64_t r, Row& a) {
-    load(p.h, r, a.h);
-    load(p.dy, r, a.dy);
-    if (p.dh) load(p.dh, r, a.dh);
+    a.h = load(p.h, r);
+    a.dy = load(p.dy, r);
+    if (p.dh) a.dh = load(p.dh, r);
   };
   const float inv_cols = 1.f / static_cast<float>(p.cols);
   Row a;
   if (row0 < p.rows) load_row(row0, a);
-  Pack16<T> w[NV];
-  load(p.weight, 0, w);
-  F2 dw[N / 2];
+  const Pack16<T> w = load(p.weight, 0);
+  F2 dw[kPairs];
 #pragma unroll
-  for (int n = 0; n < N / 2; ++n) dw[n] = f2(0.f, 0.f);
+  for (int n = 0; n < kPairs; ++n) dw[n] = f2(0.f, 0.f);
   int flip = 0;
   for (int64_t r = row0; r < p.rows; r += row_step, flip ^= 1) {
     Row next;
     if (PRE && r + row_step < p.rows) load_row(r + row_step, next);
     F2 hh = f2(0.f, 0.f), gh = hh;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
+    {
       F2 h[kPairs], dy[kPairs], g[kPairs];
-      unpack16(a.h[i], h);
-      unpack16(a.dy[i], dy);
-      unpack16(w[i], g);
+      unpack16(a.h, h);
+      unpack16(a.dy, dy);
+      unpack16(w, g);
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
         hh = f2_fma(h[j], h[j], hh);
@@ -328,62 +320,59 @@ __global__ void __launch_bounds__(SPAN == 0 ? 32 * kWarpRows : kGradThreads, SPA
     const float c = -(rstd * rstd * rstd * (s[1] * inv_cols));
     const F2 rstd2 = f2(rstd, rstd), c2 = f2(c, c);
     T* dx = static_cast<T*>(p.dx) + r * p.cols;
+    F2 h[kPairs], dy[kPairs], g[kPairs];
+    unpack16(a.h, h);
+    unpack16(a.dy, dy);
+    unpack16(w, g);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      F2 h[kPairs], dy[kPairs], g[kPairs];
-      unpack16(a.h[i], h);
-      unpack16(a.dy[i], dy);
-      unpack16(w[i], g);
+    for (int j = 0; j < kPairs; ++j) {
+      const F2 t = f2_mul(dy[j], rstd2);
+      dw[j] = f2_fma(t, h[j], dw[j]);
+      h[j] = f2_fma(h[j], c2, f2_mul(t, g[j]));
+    }
+    if (p.dh) {
+      unpack16(a.dh, g);
 #pragma unroll
-      for (int j = 0; j < kPairs; ++j) {
-        const F2 t = f2_mul(dy[j], rstd2);
-        dw[kPairs * i + j] = f2_fma(t, h[j], dw[kPairs * i + j]);
-        h[j] = f2_fma(h[j], c2, f2_mul(t, g[j]));
-      }
-      if (p.dh) {
-        unpack16(a.dh[i], g);
+      for (int j = 0; j < kPairs; ++j) h[j] = f2_add(h[j], g[j]);
+    }
+    const Pack16<T> o = pack16<T>(h);
+    if constexpr (VEC) {
+      store16<true>(dx, me, p.cols, o, static_cast<T*>(nullptr));
+    } else {
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) h[j] = f2_add(h[j], g[j]);
-      }
-      const Pack16<T> o = pack16<T>(h);
-      if constexpr (VEC) {
-        store16<true>(dx, me + static_cast<int64_t>(i) * threads, p.cols, o, static_cast<T*>(nullptr));
-      } else {
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j)
-          if (column(kChunk * i + j) < p.cols) dx[column(kChunk * i + j)] = o.e[j];
-      }
+      for (int j = 0; j < kChunk; ++j)
+        if (kStride * j < left) dx[first + kStride * j] = o.e[j];
     }
     if (PRE) a = next;
     else if (r + row_step < p.rows) load_row(r + row_step, a);
   }
-  float dws[N];
+  float dws[kChunk];
 #pragma unroll
-  for (int n = 0; n < N / 2; ++n) {
+  for (int n = 0; n < kPairs; ++n) {
     const float2 t = f2_get(dw[n]);
     dws[2 * n] = t.x, dws[2 * n + 1] = t.y;
   }
-  float* part = p.part + block * p.cols;
+  float* part = p.part + block * p.cols + first;
   if constexpr (WARP) {
     // the block's warps in their order
 #pragma unroll
-    for (int n = 0; n < N; ++n) sums[(group * N + n) * 32 + me] = dws[n];
+    for (int n = 0; n < kChunk; ++n) sums[(group * kChunk + n) * 32 + me] = dws[n];
     __syncthreads();
-    for (int n = group; n < N; n += kWarpRows) {
+    for (int n = group; n < kChunk; n += kWarpRows) {
       float t = 0.f;
 #pragma unroll
-      for (int g = 0; g < kWarpRows; ++g) t += sums[(g * N + n) * 32 + me];
-      if (column(n) < p.cols) part[column(n)] = t;
+      for (int g = 0; g < kWarpRows; ++g) t += sums[(g * kChunk + n) * 32 + me];
+      if (kStride * n < left) part[kStride * n] = t;
     }
   } else {
 #pragma unroll
-    for (int n = 0; n < N; n += 4) {
+    for (int n = 0; n < kChunk; n += 4) {
       if (VEC) {
-        if (column(n) < p.cols) *reinterpret_cast<float4*>(part + column(n)) = make_float4(dws[n], dws[n + 1], dws[n + 2], dws[n + 3]);
+        if (n < left) *reinterpret_cast<float4*>(part + n) = make_float4(dws[n], dws[n + 1], dws[n + 2], dws[n + 3]);
       } else {
 #pragma unroll
         for (int k = n; k < n + 4; ++k)
-          if (column(k) < p.cols) part[column(k)] = dws[k];
+          if (kStride * k < left) part[kStride * k] = dws[k];
       }
     }
   }
