@@ -418,30 +418,42 @@ __global__ void __launch_bounds__(1024) dbf_rmsnorm_grad_wide_kernel(const NormG
   }
 }
 
-// dweight[c] = sum over the blocks' rows of `part`, in their order.  32 columns
-// and 32 runs of rows per block: the loads' latency bounds it, so all of a
-// thread's are under way together.
-constexpr int kSumRuns = 32;
-__global__ void __launch_bounds__(32 * kSumRuns) dbf_rmsnorm_grad_sum_kernel(const NormGradArgs p) {
-  __shared__ float tile[kSumRuns][33];
+// dweight[c] = sum over the blocks' rows of `part`, in a fixed order.  A block
+// takes COLS columns by RUNS runs of rows.  The loads' latency bounds it: 296
+// rows of 4096 columns took 5 us more with 8 runs than with 64.  Narrow rows
+// need the runs most (4096 x 64: 7.0 us of the whole call with 32, 5.6 with
+// 128), wide ones the whole sectors (2048 x 8192: 27.7 with 32, 29.2 with 64).
+template <int COLS, int RUNS>
+__global__ void __launch_bounds__(COLS * RUNS) dbf_rmsnorm_grad_sum_kernel(const NormGradArgs p) {
+  __shared__ float tile[RUNS][COLS + 1];
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
-  const int64_t c = 32 * static_cast<int64_t>(blockIdx.x) + lane;
+  const int col = threadIdx.x % COLS, run = threadIdx.x / COLS;
+  const int64_t c = COLS * static_cast<int64_t>(blockIdx.x) + col;
   float s = 0.f;
   if (c < p.cols) {
     const float* part = p.part + c;
-#pragma unroll 10
-    for (int b = run; b < p.blocks; b += kSumRuns) s += part[b * p.cols];
+#pragma unroll(RUNS == 32 ? 10 : RUNS == 64 ? 5 : 4)
+    for (int b = run; b < p.blocks; b += RUNS) s += part[b * p.cols];
   }
-  tile[run][lane] = s;
+  tile[run][col] = s;
   __syncthreads();
-  // warp `run` adds column `run`'s sums
-  s = tile[lane][run];
+  // warp w adds column w's runs
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp >= COLS) return;
+  s = 0.f;
+#pragma unroll
+  for (int k = lane; k < RUNS; k += 32) s += tile[k][warp];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  const int64_t out = 32 * static_cast<int64_t>(blockIdx.x) + run;
+  const int64_t out = COLS * static_cast<int64_t>(blockIdx.x) + warp;
   if (lane == 0 && out < p.cols) p.dweight[out] = s;
+}
+
+template <int COLS, int RUNS>
+dbf_status launch_grad_sum(const NormGradArgs& a, cudaStream_t stream) {
+  return launch_pdl(dbf_rmsnorm_grad_sum_kernel<COLS, RUNS>, dim3(static_cast<unsigned>((a.cols + COLS - 1) / COLS)),
+                    dim3(COLS * RUNS), 0, stream, a);
 }
 
 // How the rows are shared out, from the sizes alone (the workspace's size and
@@ -480,8 +492,8 @@ dbf_status launch_grad(NormGradArgs a, const DeviceInfo& dev, cudaStream_t strea
     st = launch_pdl(dbf_rmsnorm_grad_wide_kernel<T>, grid, block, 0, stream, a);
   }
   if (st != DBF_OK) return st;
-  return launch_pdl(dbf_rmsnorm_grad_sum_kernel, dim3(static_cast<unsigned>((a.cols + 31) / 32)), dim3(32 * kSumRuns), 0, stream,
-                    a);
+  if (a.cols <= 2048) return launch_grad_sum<8, 128>(a, stream);
+  return a.cols <= 6144 ? launch_grad_sum<16, 64>(a, stream) : launch_grad_sum<32, 32>(a, stream);
 }
 
 template <typename T>
