@@ -61,7 +61,11 @@ __device__ __forceinline__ void store_out(void* out, int t, int64_t at, float v)
 // cluster, each of which sends its fp32 partial sums of token group g to CTA
 // g % size, which adds them in rank order.  With few tokens the weights'
 // stream bounds it; a stage of the ring is U steps, because a stage costs some
-// 250 cycles of waiting and signalling however little it multiplies.
+// 250 cycles of waiting and signalling however little it multiplies (one token x
+// 14336 x 4096, 8-bit tokens: 9.5 us with one step, 9.1 with two).
+// Measured: 4-bit weights of 4096 x 4096 / 14336 x 4096, one token in 8 bits 4.8 /
+// 9.1 us (28 / 53% of the weights' DRAM time), in 4 bits 7.6 us for the wide one;
+// 16 tokens 5.1 / 9.5 us; 128 tokens x 4096 x 4096 8.7 us.
 template <int KA, int NT>
 struct SplitCfg {
   static constexpr int U = NT <= 32 ? 2 : 1;
@@ -321,7 +325,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 // last / first columns (both do not fit beside the scales), so the MMAs of an
 // item wait only until the epilogue has read the shared columns of the one before.
 // The epilogue writes through shared memory with TMA stores (rows of y on 16
-// bytes), else row by row.
+// bytes), else row by row (n = 14335 fp16: 104 us where 14336 takes 50).
+// The issue of a step's copies, MMAs and commit by one thread takes 590 cycles,
+// its MMAs alone 512: that, the accumulators' hand-over (about 1000 cycles an
+// item) and the clock under load bound it.  Loads, stores and the copies were
+// taken out one at a time without effect.  Tried and slower: the scales written
+// by other warps with tcgen05.st (220 us for 84: it waits behind the MMAs),
+// copies by a second thread (93), 192 weight rows with no shared columns (95).
+// Measured: 2048 x 14336 x 4096, everything in 4 bits, fp16 out 49.5 us (4.86
+// PFLOP/s); 2048 x 4096 x 14336, tokens in 8 bits 82 us (2.9 PFLOP/s).
 constexpr int kPairCols = 256;  // weight rows of a whole tile
 template <int KA>
 struct PairCfg {

@@ -3,7 +3,11 @@
 //   s = clamp(floor(log2(max |x|)) - top, -127, 127) over each block of 32
 //   code = round_to_nearest_even(x 2^-s), saturating;  value = code 2^s
 //
-// Both read every input once and write every output once, so DRAM bounds them.
+// Both read every input once and write every output once, so DRAM bounds them;
+// what keeps them from its rate are the instructions (about 90 for the sixteen
+// elements of a thread).  14336 x 4096 bf16 into 4 bits 29.2 us (5.1 TB/s, 78% of
+// the copy rate), back 26.4 us (5.6 TB/s, 86%), its transpose into 4 bits 37.6 us
+// (4.0 TB/s, 61%).
 #include <algorithm>
 
 #include "dbf_internal.h"
