@@ -120,6 +120,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int k1 = static_cast<int>(static_cast<int64_t>(a.steps_k) * (rank + 1) / ks);
   const int stages = (k1 - k0 + U - 1) / U;
 
+  // The producer's thread sets up the barriers and, if the weights may be read at
+  // once, has the first ring's worth of them on its way before anyone meets.
+  auto tiles_of = [&](int k) {  // 128-element groups of the stage that starts at step k
+    return static_cast<int>(min(static_cast<int64_t>(min(U, k1 - k) * KA), a.k4s - static_cast<int64_t>(k) * KA));
+  };
+  auto load = [&](bool weights, int i) {
+    const int k = k0 + i * U, s = i % S, tiles = tiles_of(k);
+    const CUtensorMap* map = weights ? &p_map : &q_map;
+    const uint8_t* scales = weights ? a.p_scales : a.q_scales;
+    const int64_t row = weights ? p0 : q0;
+    const int bytes = weights ? C::kPBytes : C::kQBytes;
+    uint8_t* st = (weights ? p_st : q_st) + s * U * bytes;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (u == 0 || k + u < k1) tma_load_2d(st + u * bytes, map, (k + u) * 128, static_cast<int>(row), &full[s]);
+    bulk_load(s_st + (2 * s + (weights ? 0 : 1)) * C::kScaleBytes,
+              scales + ((row >> 7) * a.k4s + static_cast<int64_t>(k) * KA) * kTileBytes, tiles * kTileBytes, &full[s]);
+  };
+  auto expect = [&](int i) {
+    const int k = k0 + i * U;
+    mbar_arrive_expect_tx(&full[i % S], min(U, k1 - k) * (kRows * a.p_tx + NT * a.q_tx) + 2 * tiles_of(k) * kTileBytes);
+  };
+  const int early = min(S, stages);
   if (tid == 0) {
     prefetch_tmap(&p_map);
     prefetch_tmap(&q_map);
@@ -131,7 +154,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_barrier_init();
+    if (a.w_static) {
+      for (int i = 0; i < early; ++i) {
+        expect(i);
+        load(true, i);
+      }
+    }
   }
+  __syncwarp();
   if (warp == 1) {
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
@@ -147,37 +177,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------ TMA producer
     if (elect_one()) {
-      auto tiles_of = [&](int k) {  // 128-element groups of the stage that starts at step k
-        return static_cast<int>(min(static_cast<int64_t>(min(U, k1 - k) * KA), a.k4s - static_cast<int64_t>(k) * KA));
-      };
-      auto load = [&](bool weights, int i) {
-        const int k = k0 + i * U, s = i % S, tiles = tiles_of(k);
-        const CUtensorMap* map = weights ? &p_map : &q_map;
-        const uint8_t* scales = weights ? a.p_scales : a.q_scales;
-        const int64_t row = weights ? p0 : q0;
-        const int bytes = weights ? C::kPBytes : C::kQBytes;
-        uint8_t* st = (weights ? p_st : q_st) + s * U * bytes;
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (u == 0 || k + u < k1) tma_load_2d(st + u * bytes, map, (k + u) * 128, static_cast<int>(row), &full[s]);
-        bulk_load(s_st + (2 * s + (weights ? 0 : 1)) * C::kScaleBytes,
-                  scales + ((row >> 7) * a.k4s + static_cast<int64_t>(k) * KA) * kTileBytes, tiles * kTileBytes, &full[s]);
-      };
-      auto expect = [&](int i) {
-        const int k = k0 + i * U;
-        mbar_arrive_expect_tx(&full[i % S],
-                              min(U, k1 - k) * (kRows * a.p_tx + NT * a.q_tx) + 2 * tiles_of(k) * kTileBytes);
-      };
-      // the first ring's worth of the weights is on its way before the wait for
-      // the kernel that writes the tokens
-      const int early = min(S, stages);
-      if (!a.w_static) pdl_wait();
+      pdl_wait();
       for (int i = 0; i < early; ++i) {
-        expect(i);
-        load(true, i);
+        if (!a.w_static) {
+          expect(i);
+          load(true, i);
+        }
+        load(false, i);
       }
-      if (a.w_static) pdl_wait();
-      for (int i = 0; i < early; ++i) load(false, i);
       int it = early;
       for (; it < stages; ++it) {
         if (!mbar_wait_often<false>(&empty[it % S], (it / S - 1) & 1, abort_flag, a.status)) break;

@@ -276,3 +276,66 @@ def test_refusals_of_the_binding(dbf):
         dbf.dbf_mx_forward(codes, scales, codes, scales, 4, 64, 4, x_fmt=0, w_fmt=0, y_dtype=torch.float64)
     with pytest.raises(dbf.DBFError):
         dbf.dbf_mx_forward(codes, scales, codes, scales, 4, 64, 4, x_fmt=0, w_fmt=0, flags=1 << 5)
+
+
+def test_offsets_past_32_bits(dbf):
+    """Matrices of more than 2^31 elements: their last rows equal those rows handled alone."""
+    rows, cols = 70000, 32768
+    src = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_()
+    tail = src[-3:].contiguous()
+    for fmt in (mx.E2M1, mx.E4M3):
+        codes, scales = dbf.dbf_mx_quantize(src, fmt)
+        want = dbf.dbf_mx_dequantize(*dbf.dbf_mx_quantize(tail, fmt), 3, cols, fmt, dtype=torch.bfloat16)
+        whole = dbf.dbf_mx_dequantize(codes, scales, rows, cols, fmt, dtype=torch.bfloat16)
+        assert torch.equal(whole[-3:], want)
+        del codes, scales, whole
+    codes, scales = dbf.dbf_mx_quantize(src, mx.E2M1, transpose=True)
+    back = dbf.dbf_mx_dequantize(codes, scales, cols, rows, mx.E2M1, dtype=torch.bfloat16)
+    want = dbf.dbf_mx_dequantize(*dbf.dbf_mx_quantize(src[:, -5:].t().contiguous(), mx.E2M1), 5, rows, mx.E2M1,
+                                 dtype=torch.bfloat16)
+    assert torch.equal(back[-5:], want)
+    del codes, scales, back
+    w = torch.ones(cols, dtype=torch.bfloat16, device="cuda")
+    y, _ = dbf.dbf_rmsnorm_forward(src, w, 1e-5)
+    assert torch.equal(y[-3:], dbf.dbf_rmsnorm_forward(tail, w, 1e-5)[0])
+    dx, _ = dbf.dbf_rmsnorm_backward(y, src, w, 1e-5, dx=y)
+    assert torch.equal(dx[-3:], dbf.dbf_rmsnorm_backward(dbf.dbf_rmsnorm_forward(tail, w, 1e-5)[0], tail, w, 1e-5)[0])
+
+
+@pytest.mark.parametrize("n", [60000, 60001])
+def test_results_past_32_bits(dbf, n):
+    batch, m_in = 40000, 130
+    g = torch.Generator(device="cuda").manual_seed(3)
+    X, W = (torch.randn(r, m_in, generator=g, device="cuda") for r in (batch, n))
+    x, w = dbf.dbf_mx_quantize(X, mx.E4M3), dbf.dbf_mx_quantize(W, mx.E2M1)
+    y = dbf.dbf_mx_forward(*x, *w, n, m_in, batch)
+    xs, ws = host(X)[-300:], host(W)[-500:]
+    assert_product(y[-300:, -500:], xs, ws, mx.E4M3, mx.E2M1, "fp16")
+    assert_product(y[:5, :300], host(X)[:5], host(W)[:300], mx.E4M3, mx.E2M1, "fp16")
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_sizes(dbf, seed):
+    """Sizes, formats and result types at random, the split and the pair kernel among them."""
+    rng = np.random.default_rng(100 + seed)
+    size = lambda low, high: int(round(low * (high / low) ** rng.random()))  # noqa: E731
+    batch, n, m_in = size(1, 2000), size(1, 6000), size(1, 3000)
+    xf, wf = FORMATS[rng.integers(4)]
+    kind = ["fp16", "bf16", "fp32"][rng.integers(3)]
+    X, W = rng.standard_normal((batch, m_in)), rng.standard_normal((n, m_in)) * 0.1
+    assert_product(product(dbf, X, W, xf, wf, kind), X, W, xf, wf, kind)
+
+
+def test_a_call_behind_one_that_writes_its_operands(dbf):
+    """Quantisation and product back to back on one stream, without the static flag: the product waits for the weights."""
+    rng = np.random.default_rng(21)
+    src = [torch.from_numpy(rng.standard_normal((2048, 1024))).to(torch.bfloat16).cuda() for _ in range(2)]
+    X = held(rng.standard_normal((16, 1024)), mx.E4M3)
+    codes, scales = (torch.empty_like(t) for t in dbf.dbf_mx_quantize(src[0], mx.E2M1))
+    ws = dbf.dbf_mx_new_workspace(2048, 1024, 16)
+    want = [dbf.dbf_mx_forward(*X, *dbf.dbf_mx_quantize(s, mx.E2M1), 2048, 1024, 16) for s in src]
+    torch.cuda.synchronize()
+    for i in range(40):
+        dbf.dbf_mx_quantize(src[i % 2], mx.E2M1, codes=codes, scales=scales)
+        y = dbf.dbf_mx_forward(*X, codes, scales, 2048, 1024, 16, workspace=ws)
+        assert torch.equal(y, want[i % 2])

@@ -252,3 +252,18 @@ def test_refusals_of_the_binding(dbf):
                 lambda: dbf.dbf_rmsnorm_backward(r, x, w, EPS, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(dbf.DBFError):
             bad()
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_sizes(dbf, seed):
+    rng = np.random.default_rng(200 + seed)
+    size = lambda low, high: int(round(low * (high / low) ** rng.random()))  # noqa: E731
+    rows, cols, kind = size(1, 400), size(1, 20000), ["fp16", "bf16", "fp32"][rng.integers(3)]
+    x, r, w = data(rows, cols, kind, seed=seed)
+    y, h = dbf.dbf_rmsnorm_forward(x, w, EPS, residual=r)
+    assert_dense(y, h, w, EPS, kind)
+    fmt = [mx.E2M1, mx.E4M3][rng.integers(2)]
+    codes, scales, _ = dbf.dbf_rmsnorm_mx_forward(x, w, EPS, fmt, residual=r)
+    assert_quantised(codes, scales, h, w, EPS, fmt)
+    dx, dw = dbf.dbf_rmsnorm_backward(y, h, w, EPS, dh=r)
+    assert_grads(dx, dw, y, h, w, r, kind)
