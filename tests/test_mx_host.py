@@ -28,7 +28,7 @@ def test_sizes(lib):
     assert dbf.dbf_mx_code_bytes((1 << 24) + 1, 4, 0) == 0
     assert dbf.dbf_mx_forward_workspace_bytes(4096, 4096, 1) >= 256
     assert dbf.dbf_mx_forward_workspace_bytes(4096, (1 << 20) + 1, 1) == 0
-    assert dbf.dbf_rmsnorm_backward_workspace_bytes(2, 4096) == 2 * 4096 * 4
+    assert dbf.dbf_rmsnorm_backward_workspace_bytes(2000, 4096) >= 4096 * 4
     assert dbf.dbf_rmsnorm_backward_workspace_bytes(0, 4096) == 0
 
 
