@@ -276,6 +276,17 @@ __device__ __forceinline__ Pack16<T> load16(const T* row, int64_t c, int64_t col
   return p;
 }
 
+// The same of one row that starts on 32 bytes, whatever its length (a weight
+// vector): whole chunks in vectors, the last one by elements.
+template <typename T>
+__device__ __forceinline__ Pack16<T> load16_aligned(const T* row, int64_t c, int64_t cols) {
+  if (kChunk * (c + 1) <= cols) return load16<true>(row, c, cols, static_cast<T*>(nullptr));
+  Pack16<T> p;
+#pragma unroll
+  for (int j = 0; j < kChunk; ++j) p.e[j] = kChunk * c + j < cols ? row[kChunk * c + j] : from_f32<T>(0.f);
+  return p;
+}
+
 template <bool VEC, typename T>
 __device__ __forceinline__ void store16(T* row, int64_t c, int64_t cols, const Pack16<T>& p, T* stage) {
   if constexpr (VEC) {

@@ -30,6 +30,7 @@ struct NormArgs {
   uint8_t* scales;
   int64_t rows, cols, pitch;  // pitch: columns padded to 128 (MX output) or 8 (dense)
   float eps;
+  int weight_aligned;  // to 32 bytes
 };
 
 // Sum of one value per thread over the row's threads (every thread gets it):
@@ -70,6 +71,10 @@ __global__ void __launch_bounds__(VEC && !WARP ? 1024 : kStagedThreads) dbf_rmsn
   const int me = WARP ? threadIdx.x & 31 : threadIdx.x, threads = WARP ? 32 : blockDim.x;
   const int64_t row_step = static_cast<int64_t>(gridDim.x) * (WARP ? kWarpRows : 1);
   const float inv_cols = 1.f / static_cast<float>(p.cols);
+  auto load_weight = [&](int64_t c) {
+    if (!VEC && p.weight_aligned) return load16_aligned(weight, c, p.cols);
+    return load16<VEC>(weight, c, p.cols, stage);
+  };
   int flip = 0;
   for (int64_t r = WARP ? static_cast<int64_t>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x; r < p.rows;
        r += row_step, flip ^= 1) {
@@ -125,7 +130,7 @@ __global__ void __launch_bounds__(VEC && !WARP ? 1024 : kStagedThreads) dbf_rmsn
         if (rr) b[i] = load16<VEC>(rr, c, p.cols, stage);
       }
 #pragma unroll
-      for (int i = 0; i < NV; ++i) w[i] = load16<VEC>(weight, me + i * threads, p.cols, stage);
+      for (int i = 0; i < NV; ++i) w[i] = load_weight(me + i * threads);
 #pragma unroll
       for (int i = 0; i < NV; ++i) a[i] = add(me + i * threads, a[i], b[i]);
       const float rstd = rstd_of();
@@ -143,7 +148,7 @@ __global__ void __launch_bounds__(VEC && !WARP ? 1024 : kStagedThreads) dbf_rmsn
       const T* again = rr ? hr : xr;
       for (int64_t i = 0; i < rounds; ++i) {
         const int64_t c = me + i * threads;
-        finish(c, load16<VEC>(again, c, p.cols, stage), load16<VEC>(weight, c, p.cols, stage), rstd);
+        finish(c, load16<VEC>(again, c, p.cols, stage), load_weight(c), rstd);
       }
     }
   }
@@ -175,9 +180,11 @@ dbf_status launch_norm(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st
 
 template <typename T, int OUT>
 dbf_status norm_typed(const NormArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
+  NormArgs args = a;
+  args.weight_aligned = aligned_to(a.weight, 32);
   const bool vec = a.cols % kChunk == 0 && aligned_to(a.x, 32) && aligned_to(a.residual, 32) &&
                    aligned_to(a.weight, 32) && aligned_to(a.h, 32) && aligned_to(a.y, 32);
-  return vec ? launch_norm<T, OUT, true>(a, dev, stream) : launch_norm<T, OUT, false>(a, dev, stream);
+  return vec ? launch_norm<T, OUT, true>(args, dev, stream) : launch_norm<T, OUT, false>(args, dev, stream);
 }
 
 template <int OUT>
@@ -563,7 +570,7 @@ extern "C" {
 
 dbf_status dbf_rmsnorm_forward(const void* x, const void* residual, const void* weight, dbf_dtype t, int64_t rows,
                                int64_t cols, float eps, void* h, void* y, struct CUstream_st* stream) {
-  NormArgs a{x, residual, weight, h, y, nullptr, nullptr, rows, cols, cols, eps};
+  NormArgs a{x, residual, weight, h, y, nullptr, nullptr, rows, cols, cols, eps, 0};
   if (!y) return DBF_ERR_INVALID_ARG;
   dbf_status st = check_norm(a, t);
   if (st != DBF_OK) return st;
@@ -577,7 +584,7 @@ dbf_status dbf_rmsnorm_forward(const void* x, const void* residual, const void* 
 dbf_status dbf_rmsnorm_mx_forward(const void* x, const void* residual, const void* weight, dbf_dtype t, int64_t rows,
                                   int64_t cols, float eps, dbf_mx_format fmt, void* h, uint8_t* codes, uint8_t* scales,
                                   struct CUstream_st* stream) {
-  NormArgs a{x, residual, weight, h, nullptr, codes, scales, rows, cols, cols, eps};
+  NormArgs a{x, residual, weight, h, nullptr, codes, scales, rows, cols, cols, eps, 0};
   if (!codes || !scales || !mx_format_ok(fmt)) return DBF_ERR_INVALID_ARG;
   dbf_status st = check_norm(a, t);
   if (st != DBF_OK) return st;
@@ -599,7 +606,7 @@ dbf_status dbf_rmsnorm_backward(const void* dy, const void* h, const void* weigh
                                 int64_t rows, int64_t cols, float eps, void* dx, float* dweight, void* workspace,
                                 size_t ws_bytes, struct CUstream_st* stream) {
   if (!dy || !dx || !dweight) return DBF_ERR_INVALID_ARG;
-  NormArgs check{h, nullptr, weight, nullptr, nullptr, nullptr, nullptr, rows, cols, cols, eps};
+  NormArgs check{h, nullptr, weight, nullptr, nullptr, nullptr, nullptr, rows, cols, cols, eps, 0};
   dbf_status st = check_norm(check, t);
   if (st != DBF_OK) return st;
   const size_t e = dtype_size(t);
