@@ -357,3 +357,37 @@ def test_bench_mode_runs():
     for r in rows:
         for b in (1, 16, 128, 2048):
             assert r[f"product_us_b{b}"] > 0 and 0.05 < r[f"rel_error_b{b}"] < 0.2
+
+
+def test_first_calls_inside_a_capture(dbf):
+    """A process whose first calls of every operator are captured: nothing needs a call before."""
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import torch
+import binary_factorized_weight_b200 as dbf
+W = torch.randn(4096, 512, device="cuda"); x = torch.randn(600, 512, device="cuda"); w = torch.ones(512, device="cuda")
+ws = dbf.dbf_mx_new_workspace(4096, 512, 600)
+torch.cuda.synchronize()
+def run():
+    q = dbf.dbf_mx_quantize(W, 0)
+    t = dbf.dbf_mx_quantize(W, 1, transpose=True)
+    c, s, h = dbf.dbf_rmsnorm_mx_forward(x, w, 1e-5, 1, residual=x)
+    y = dbf.dbf_mx_forward(c, s, *q, 4096, 512, 600, workspace=ws, y_dtype=torch.float32)
+    few = dbf.dbf_mx_quantize(x[:5].contiguous(), 1)
+    z = dbf.dbf_mx_forward(*few, *q, 4096, 512, 5, workspace=ws, y_dtype=torch.float32)
+    dx, dw = dbf.dbf_rmsnorm_backward(x, h, w, 1e-5)
+    return y, z, dx, dw, dbf.dbf_mx_dequantize(*t, 512, 4096, 1), dbf.dbf_rmsnorm_forward(x, w, 1e-5)[0]
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = run()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, run())) and dbf.dbf_workspace_status(ws) == 0
+print("same")
+"""
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=200)
+    assert out.returncode == 0 and out.stdout.strip().endswith("same"), out.stderr[-2000:]
