@@ -63,9 +63,9 @@ __device__ __forceinline__ void store_out(void* out, int t, int64_t at, float v)
 // stream bounds it; a stage of the ring is U steps, because a stage costs some
 // 250 cycles of waiting and signalling however little it multiplies (one token x
 // 14336 x 4096, 8-bit tokens: 9.5 us with one step, 9.1 with two).
-// Measured: 4-bit weights of 4096 x 4096 / 14336 x 4096, one token in 8 bits 4.8 /
-// 9.1 us (28 / 53% of the weights' DRAM time), in 4 bits 7.6 us for the wide one;
-// 16 tokens 5.1 / 9.5 us; 128 tokens x 4096 x 4096 8.7 us.
+// Measured: 4-bit weights of 4096 x 4096 / 14336 x 4096, one token in 8 bits 4.6 /
+// 9.1 us (the weights' DRAM time is 30 / 53% of that), in 4 bits 7.7 us for the wide
+// one; 16 tokens 5.1 / 9.5 us; 128 tokens x 4096 x 4096 8.6 us.
 template <int KA, int NT>
 struct SplitCfg {
   static constexpr int U = NT <= 32 ? 2 : 1;
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // last / first columns (both do not fit beside the scales), so the MMAs of an
 // item wait only until the epilogue has read the shared columns of the one before.
 // The epilogue writes through shared memory with TMA stores (rows of y on 16
-// bytes), else row by row (n = 14335 fp16: 104 us where 14336 takes 50).
+// bytes), else row by row (n = 14335 fp16: 101 us where 14336 takes 50).
 // The issue of a step's copies, MMAs and commit by one thread takes 590 cycles,
 // its MMAs alone 512: that, the accumulators' hand-over (about 1000 cycles an
 // item) and the clock under load bound it.  Loads, stores and the copies were
@@ -384,6 +384,25 @@ struct PairArgs {
   int tma_out;
   int* status;
 };
+
+// Rows of y that do not start on 16 bytes, from the swizzled 32 x 32 chunk in
+// shared memory: a lane per column, sixteen rows under way together.
+template <typename E>
+__device__ __forceinline__ void store_rows(const uint8_t* src, E* out, int64_t ld, int rows, int lane) {
+  constexpr int kLine = 32 * sizeof(E), kPer = 16 / sizeof(E);  // bytes of a row, elements of a 16-byte chunk
+#pragma unroll
+  for (int r0 = 0; r0 < 32; r0 += 16) {
+    E e[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int rr = r0 + k, key = sizeof(E) == 4 ? rr & 7 : (rr >> 1) & 3;
+      e[k] = *reinterpret_cast<const E*>(src + rr * kLine + (((lane / kPer) ^ key) << 4) + (lane % kPer) * sizeof(E));
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (r0 + k < rows) out[(r0 + k) * ld] = e[k];
+  }
+}
 
 template <int KA>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -614,26 +633,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ++stores;
         } else {
-          // rows of y that do not start on 16 bytes: a lane per column, eight rows under way
           __syncwarp();
-          const bool in = q0 + c0 + lane < a.q_rows;
           const int64_t at = row0 * a.ld_out + q0 + c0 + lane;
-          for (int r = 0; r < rows; r += 8) {
-            uint32_t e[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int rr = r + k;
-              e[k] = a.out_t == DBF_F32
-                         ? *reinterpret_cast<const uint32_t*>(dst + rr * 128 + (((lane >> 2) ^ (rr & 7)) << 4) + 4 * (lane & 3))
-                         : *reinterpret_cast<const uint16_t*>(dst + rr * 64 + (((lane >> 3) ^ ((rr >> 1) & 3)) << 4) +
-                                                              2 * (lane & 7));
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              if (!in || r + k >= rows) continue;
-              if (a.out_t == DBF_F32) static_cast<uint32_t*>(a.out)[at + (r + k) * a.ld_out] = e[k];
-              else static_cast<uint16_t*>(a.out)[at + (r + k) * a.ld_out] = static_cast<uint16_t>(e[k]);
-            }
+          if (q0 + c0 + lane < a.q_rows) {
+            if (a.out_t == DBF_F32) store_rows<uint32_t>(dst, static_cast<uint32_t*>(a.out) + at, a.ld_out, rows, lane);
+            else store_rows<uint16_t>(dst, static_cast<uint16_t*>(a.out) + at, a.ld_out, rows, lane);
           }
           __syncwarp();
         }
