@@ -1,5 +1,5 @@
 // Device helpers of the microscaled (MX) formats and of the kernels that read
-// or write 16-bit and fp32 rows eight elements at a time.
+// or write 16-bit and fp32 rows sixteen elements at a time.
 //
 // OCP Microscaling Formats (MX) v1.0: 32 neighbouring elements share a power of
 // two 2^(s - 127), s one byte (255: NaN).  The layouts are those of
