@@ -533,7 +533,7 @@ DBF_API dbf_status dbf_mx_forward(const uint8_t* x_codes, const uint8_t* x_scale
  * dbf_rmsnorm_forward writes y (rows x cols, type t), the input of
  * dbf_forward; dbf_rmsnorm_mx_forward quantises y as dbf_mx_quantize does
  * (without rounding it to t first), the X of dbf_mx_forward.
- * fp32 rows whose squares overflow fp32 normalise to 0 (or NaN).
+ * Rows (bf16 or fp32) whose squares overflow an fp32 sum normalise to 0 (or NaN).
  * Pointers aligned to their element (codes 32, scales 16 bytes).
  * Shape: rows in [1, 1 << 24], cols in [1, 1 << 20], at most 2^40 elements.
  */
@@ -549,6 +549,8 @@ DBF_API dbf_status dbf_rmsnorm_mx_forward(const void* x, const void* residual, c
  * With rstd = 1 / sqrt(mean(h^2) + eps) and g = dy weight:
  *     dx = rstd g - h rstd^3 mean(g h) + dh      (x's and the residual's gradient)
  *     dweight = sum over rows of dy h rstd
+ * Accurate for every eps that is accepted and rows whose sums of squares and of g h
+ * fit fp32; a row whose squares overflow has rstd = 0.
  *   dy, h, dh, dx   rows x cols of type t; dh, the gradient that reaches h by the
  *              residual stream, may be null.  dx may be dh or dy; no other overlap.
  *   dweight    cols fp32 (the sum's order is fixed by the sizes).

@@ -267,3 +267,48 @@ def test_random_sizes(dbf, seed):
     assert_quantised(codes, scales, h, w, EPS, fmt)
     dx, dw = dbf.dbf_rmsnorm_backward(y, h, w, EPS, dh=r)
     assert_grads(dx, dw, y, h, w, r, kind)
+
+
+# ---------------------------------------------------------------- the ends of the range
+# Few rows (one cluster), a warp's rows (aligned and not), a block's, a cluster's, and rows of any width.
+GRAD_FORMS = [(5, 256), (5, 4095), (40, 512), (40, 333), (40, 4096), (40, 1000), (40, 9008), (24, 20001), (5, 65537)]
+
+
+@pytest.mark.parametrize("eps", [1e-5, 1e-30, 1.2e-38])
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,cols", GRAD_FORMS)
+def test_backward_of_special_rows(dbf, rows, cols, kind, eps):
+    """Rows of zeros, of large and of small values, at every eps that the calls take.  The tolerance is assert_grads':
+    it counts relative roundings only, so it holds as long as no intermediate leaves the normal range, and here the
+    squares (up to 65537 * 2^4 * 1e30 < 1e37) and quotients (1 / sqrt(1.2e-38) < 1e20) are far from its ends."""
+    h, dy, w = data(rows, cols, kind, seed=12)
+    dh = data(rows, cols, kind, seed=13)[0]
+    h[0] = 0
+    h[1] *= 1e15
+    h[2] *= 1e-18
+    h[3] *= 1e13
+    a, b, c = host(dy), host(h), host(w)
+    r = 1 / np.sqrt((b * b).mean(1, keepdims=True) + eps)
+    g, d = np.abs(a * c), 4 * rel(cols)
+    size = r * g + r * np.abs(b * r) * (g * np.abs(b * r)).mean(1, keepdims=True)
+    for extra in (None, dh):
+        dx, dw = dbf.dbf_rmsnorm_backward(dy, h, w, eps, dh=extra)
+        want_dx, want_dw = mx.rmsnorm_grads(a, b, c, eps, None if extra is None else host(extra))
+        tol = 2 * d * size + STEP[kind] * np.abs(want_dx) + TINY[kind]
+        tol = (tol + (0 if extra is None else U * np.abs(host(extra)) + U * size)) * (1 + STEP[kind])
+        assert (np.abs(host(dx) - want_dx) <= tol).all(), np.nanmax(np.abs(host(dx) - want_dx) / tol, axis=1)[:5]
+        tol = ((rows + 320) * U + d) * (np.abs(a * b) * r).sum(0)
+        assert (np.abs(host(dw) - want_dw) <= tol).all()
+
+
+@pytest.mark.parametrize("rows,cols", GRAD_FORMS)
+def test_backward_of_rows_with_nan_and_infinity(dbf, rows, cols):
+    """They make their own rows and, through the sum over rows, dweight NaN; the other rows are as without them."""
+    h, dy, w = data(rows, cols, "fp32", seed=14)
+    want, _ = dbf.dbf_rmsnorm_backward(dy, h, w, EPS)
+    h[1, cols // 2] = float("nan")
+    h[3, cols - 1] = float("inf")
+    dx, dw = dbf.dbf_rmsnorm_backward(dy, h, w, EPS)
+    assert torch.isnan(dx[[1, 3]]).all() and torch.isnan(dw).all()
+    keep = [i for i in range(rows) if i not in (1, 3)]
+    assert torch.equal(dx[keep], want[keep])
