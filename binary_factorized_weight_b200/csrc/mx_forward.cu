@@ -315,7 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    (void)mbar_wait_often<false>(mma_done, 0, abort_flag, a.status);
+    int never = 0;  // the MMAs under way are waited for after a wait that gave up, too
+    (void)mbar_wait_often<false>(mma_done, 0, &never, a.status);
     __syncwarp();
     tmem_dealloc(tmem, C::kTmemCols);
   }
@@ -666,9 +667,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ------------------------------------------------ teardown
+  // Warp 1 waits for the last MMAs: the even CTA's has issued them, the odd CTA's has
+  // been here since the start and gets a wait's limit for each of its items (a barrier
+  // with this CTA's other roles instead cost 0.4 us a launch).  After a wait that gave
+  // up the MMAs under way are waited for all the same, with a limit of their own.
   __syncwarp();
   tc_fence_before();
-  if (warp == 1) (void)mbar_wait_often<true>(mma_done, 0, abort_flag, a.status);
+  if (warp == 1) {
+    bool done = false;
+    if (rank == 1) {
+      pdl_wait();
+      for (int64_t t = pair; t < items && !done && !*abort_flag; t += pairs) {
+        int never = 0;
+        done = mbar_wait_often<true>(mma_done, 0, &never, nullptr);
+      }
+    }
+    int never = 0;
+    if (!done) (void)mbar_wait_often<true>(mma_done, 0, &never, a.status);
+    __syncwarp();
+  }
   // neither CTA ends while the other may still read its memory or signal it
   cluster_arrive_release();
   cluster_wait_acquire();

@@ -391,3 +391,28 @@ print("same")
 """
     out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=200)
     assert out.returncode == 0 and out.stdout.strip().endswith("same"), out.stderr[-2000:]
+
+
+def test_a_product_longer_than_the_limit_of_a_wait(dbf):
+    """8.6e14 operations, about 0.3 s: a bounded wait (0.2 s) covers a step or an item of a kernel, never all of it.
+    Ones with a scale for each row (of 128 in turn), so that y is known exactly: 2^17 times two powers of two."""
+    n, m_in = 57344, 1 << 17
+    row = torch.arange(128, device="cuda")
+    at = torch.arange(512, device="cuda")  # the tile's byte 16 (r % 32) + 4 (r / 32) + k belongs to row r
+    row_of = at // 16 + 32 * (at % 16 // 4)
+
+    def operand(fmt, exponent):
+        codes = torch.full((dbf.dbf_mx_code_bytes(n, m_in, fmt),), 0x22 if fmt == mx.E2M1 else 0x38, dtype=torch.uint8,
+                           device="cuda")
+        tiles = (127 + exponent[row_of]).to(torch.uint8)
+        return codes, tiles.repeat(dbf.dbf_mx_scale_bytes(n, m_in) // 512)
+
+    ex, ew = row % 7 - 3, row % 5 - 2
+    x, w = operand(mx.E4M3, ex), operand(mx.E2M1, ew)
+    y = torch.zeros(n, n, dtype=torch.bfloat16, device="cuda")
+    ws = dbf.dbf_mx_new_workspace(n, m_in, n)
+    want = torch.exp2((17 + ex[:, None] + ew[None, :]).double()).to(torch.bfloat16)
+    for _ in range(2):
+        dbf.dbf_mx_forward(*x, *w, n, m_in, n, y=y, workspace=ws)
+    assert dbf.dbf_workspace_status(ws) == 0
+    assert (y.view(n // 128, 128, n // 128, 128) == want[None, :, None, :]).all()
