@@ -107,6 +107,9 @@ __global__ void __launch_bounds__(VEC && !WARP ? 1024 : kStagedThreads) dbf_rmsn
       F2 v[kPairs], g[kPairs];
       unpack16(a, v);
       unpack16(w, g);
+      // A NaN rstd would make NaN of the zeros behind the last column, and with them
+      // of blocks that hold nothing.  (A block that holds a column is NaN then.)
+      if (OUT != kDense && kChunk * c >= p.cols) rstd = 0.f;
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) v[j] = f2_mul(f2_mul(v[j], f2(rstd, rstd)), g[j]);
       if constexpr (OUT == kDense) {

@@ -312,3 +312,20 @@ def test_backward_of_rows_with_nan_and_infinity(dbf, rows, cols):
     assert torch.isnan(dx[[1, 3]]).all() and torch.isnan(dw).all()
     keep = [i for i in range(rows) if i not in (1, 3)]
     assert torch.equal(dx[keep], want[keep])
+
+
+@pytest.mark.parametrize("fmt", [mx.E2M1, mx.E4M3])
+@pytest.mark.parametrize("rows,cols", [(6, 33), (6, 16), (200, 528), (6, 1000), (200, 1001), (6, 17000), (6, 40001), (6, 40016)])
+def test_padding_behind_rows_with_nan(dbf, rows, cols, fmt):
+    """Blocks that lie wholly behind the last column are zero, with a NaN in the row (its own blocks are NaN, as
+    dbf_mx_quantize makes them) or an infinity less an infinity."""
+    x, r, w = data(rows, cols, "fp32", seed=15)
+    x[1, cols // 3] = float("nan")
+    x[3, 2], r[4, 2], x[4, 2] = float("inf"), float("-inf"), float("inf")
+    for residual in (None, r):
+        codes, scales, _ = dbf.dbf_rmsnorm_mx_forward(x, w, EPS, fmt, residual=residual)
+        own = -(-cols // 32)
+        byte, code = mx.unpack_scales(host(scales), rows, cols), mx.unpack_codes(host(codes), rows, cols, fmt)
+        assert (byte[:, own:] == 0).all() and (code[:, cols:] == 0).all()
+        bad = [1] if residual is None else [1, 4]
+        assert (byte[bad, :own] == 255).all() and (byte[[0, 2, 5], :own] < 255).all()
