@@ -500,8 +500,10 @@ DBF_API dbf_status dbf_mx_dequantize(const uint8_t* codes, const uint8_t* scales
 
 /*
  * y = X W^T of two MX matrices: X batch x m_in, W n x m_in, each in either
- * format, on the block-scaled tensor cores (fp32 sums of exact products, the
- * order of additions fixed by the sizes).  One token to whole prompts.
+ * format, on the block-scaled tensor cores (fp32 sums of exact products; the
+ * order of additions follows from the sizes, the formats, y_t and the GPU, so a
+ * call repeats bit for bit, while another y_t or another GPU may add in another
+ * order).  One token to whole prompts.
  *   y          batch x n row-major, y_t DBF_F16, DBF_BF16 or DBF_F32; 16-byte
  *              aligned.  A NaN block makes every output of its row NaN.
  *   workspace  dbf_mx_forward_workspace_bytes(n, m_in, batch) bytes, zero-filled
