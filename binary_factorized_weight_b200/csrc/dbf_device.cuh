@@ -412,8 +412,10 @@ __device__ __forceinline__ void tc_mma_mxf8f6f4(uint32_t d_tmem, uint64_t adesc,
 }
 
 // 32 rows x 16 bytes of shared memory -> 4 columns of all four lane quadrants
-// (row i to lanes i, 32 + i, 64 + i, 96 + i).  Runs in order with this thread's
-// tcgen05.mma.
+// (row i to lanes i, 32 + i, 64 + i, 96 + i).  MMAs issued behind it by this thread
+// see what it brought.  It does NOT wait for MMAs issued before it: columns that they
+// read are overwritten under them, so a place is free again only after a
+// tcgen05.commit that covers its readers has arrived.
 __device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t sdesc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
