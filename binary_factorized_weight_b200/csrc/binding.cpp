@@ -7,6 +7,7 @@
 //
 // The entry points are given as addresses by the module that loaded libdbf
 // (init), so there is one library, the one that is loaded.
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
@@ -144,8 +145,8 @@ PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F f) {
     return f();
   } catch (const Refused&) {
     return nullptr;
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (const std::exception&) {  // the types that torch's own calls raise (OutOfMemoryError, ..)
+    torch::translate_exception_to_python(std::current_exception());
     return nullptr;
   }
 }

@@ -416,3 +416,11 @@ def test_a_product_longer_than_the_limit_of_a_wait(dbf):
         dbf.dbf_mx_forward(*x, *w, n, m_in, n, y=y, workspace=ws)
     assert dbf.dbf_workspace_status(ws) == 0
     assert (y.view(n // 128, 128, n // 128, 128) == want[None, :, None, :]).all()
+
+
+def test_out_of_memory_is_torchs_error(dbf):
+    """y of 2^40 elements from small operands: the allocator's error comes through as it is."""
+    codes, scales = dbf.dbf_mx_quantize(torch.zeros(1 << 20, 1, dtype=torch.float16, device="cuda"), mx.E2M1)
+    with pytest.raises(torch.OutOfMemoryError):
+        dbf.dbf_mx_forward(codes, scales, codes, scales, 1 << 20, 1, 1 << 20, x_fmt=mx.E2M1, w_fmt=mx.E2M1)
+    dbf.dbf_mx_quantize(torch.zeros(2, 2, device="cuda"), mx.E2M1)
