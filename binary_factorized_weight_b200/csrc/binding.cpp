@@ -97,6 +97,15 @@ void check_like(const at::Tensor& t, at::ScalarType type, int64_t numel, const c
 at::Tensor empty(at::IntArrayRef size, at::ScalarType type, const at::Tensor& like) {
   return at::empty(size, like.options().dtype(type).requires_grad(false));
 }
+// A C entry point (none throws), without the interpreter's lock: a launch may wait
+// for room in the GPU's queue, and other Python threads run meanwhile.
+template <typename... Want, typename... Given>
+dbf_status unlocked(dbf_status (*call)(Want...), Given... args) {
+  PyThreadState* const held = PyEval_SaveThread();
+  const dbf_status st = call(args...);
+  PyEval_RestoreThread(held);
+  return st;
+}
 CUstream_st* stream() { return reinterpret_cast<CUstream_st*>(c10::cuda::getCurrentCUDAStream().stream()); }
 
 void check_status(const char* name, dbf_status st) {
@@ -164,9 +173,9 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t rows = src.size(0), cols = src.size(1);
     mx_buffers(transpose ? cols : rows, transpose ? rows : cols, fmt, src, codes, scales);
     check_status("dbf_mx_quantize",
-                 p_quantize(src.data_ptr(), t, rows, cols, static_cast<dbf_mx_format>(fmt),
-                            transpose ? DBF_MX_TRANSPOSE : 0u, static_cast<uint8_t*>(codes->data_ptr()),
-                            static_cast<uint8_t*>(scales->data_ptr()), stream()));
+                 unlocked(p_quantize, src.data_ptr(), t, rows, cols, static_cast<dbf_mx_format>(fmt),
+                          transpose ? DBF_MX_TRANSPOSE : 0u, static_cast<uint8_t*>(codes->data_ptr()),
+                          static_cast<uint8_t*>(scales->data_ptr()), stream()));
     return pair(wrap(*codes), wrap(*scales));
   });
 }
@@ -184,8 +193,9 @@ PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!dst) dst = empty({rows, cols}, dtype(a[6]), codes);
     else if (dst->numel() != rows * cols) refuse(PyExc_ValueError, "dst must have rows * cols elements");
     check_status("dbf_mx_dequantize",
-                 p_dequantize(static_cast<const uint8_t*>(codes.data_ptr()), static_cast<const uint8_t*>(scales.data_ptr()),
-                              rows, cols, static_cast<dbf_mx_format>(fmt), dst->data_ptr(), t, stream()));
+                 unlocked(p_dequantize, static_cast<const uint8_t*>(codes.data_ptr()),
+                          static_cast<const uint8_t*>(scales.data_ptr()), rows, cols, static_cast<dbf_mx_format>(fmt),
+                          dst->data_ptr(), t, stream()));
     return wrap(*dst);
   });
 }
@@ -206,10 +216,11 @@ PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     else if (y->numel() != batch * n) refuse(PyExc_ValueError, "y must have batch * n elements");
     if (!work) work = at::zeros({static_cast<int64_t>(p_forward_ws(n, m_in, batch))}, xc.options());
     check_status("dbf_mx_forward",
-                 p_forward(static_cast<const uint8_t*>(xc.data_ptr()), static_cast<const uint8_t*>(xs.data_ptr()),
-                           static_cast<dbf_mx_format>(xf), static_cast<const uint8_t*>(wc.data_ptr()),
-                           static_cast<const uint8_t*>(ws.data_ptr()), static_cast<dbf_mx_format>(wf), n, m_in, batch,
-                           y->data_ptr(), t, work->data_ptr(), work->nbytes(), static_cast<uint32_t>(flags), stream()));
+                 unlocked(p_forward, static_cast<const uint8_t*>(xc.data_ptr()),
+                          static_cast<const uint8_t*>(xs.data_ptr()), static_cast<dbf_mx_format>(xf),
+                          static_cast<const uint8_t*>(wc.data_ptr()), static_cast<const uint8_t*>(ws.data_ptr()),
+                          static_cast<dbf_mx_format>(wf), n, m_in, batch, y->data_ptr(), t, work->data_ptr(),
+                          work->nbytes(), static_cast<uint32_t>(flags), stream()));
     return wrap(*y);
   });
 }
@@ -246,8 +257,9 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (y) check_like(*y, m.x.scalar_type(), m.rows * m.cols, "y must be like x");
     else y = empty({m.rows, m.cols}, m.x.scalar_type(), m.x);
     m.make_h();
-    check_status("dbf_rmsnorm_forward", p_norm(m.x.data_ptr(), data(m.residual), m.weight.data_ptr(), m.t, m.rows, m.cols,
-                                               eps, data(m.h), y->data_ptr(), stream()));
+    check_status("dbf_rmsnorm_forward",
+                 unlocked(p_norm, m.x.data_ptr(), data(m.residual), m.weight.data_ptr(), m.t, m.rows, m.cols, eps,
+                          data(m.h), y->data_ptr(), stream()));
     PyObject* h = m.h ? wrap(*m.h) : (Py_INCREF(a[0]), a[0]);
     return pair(wrap(*y), h);
   });
@@ -264,9 +276,9 @@ PyObject* norm_mx(PyObject*, PyObject* const* a, Py_ssize_t n) {
     mx_buffers(m.rows, m.cols, fmt, m.x, codes, scales);
     m.make_h();
     check_status("dbf_rmsnorm_mx_forward",
-                 p_norm_mx(m.x.data_ptr(), data(m.residual), m.weight.data_ptr(), m.t, m.rows, m.cols, eps,
-                           static_cast<dbf_mx_format>(fmt), data(m.h), static_cast<uint8_t*>(codes->data_ptr()),
-                           static_cast<uint8_t*>(scales->data_ptr()), stream()));
+                 unlocked(p_norm_mx, m.x.data_ptr(), data(m.residual), m.weight.data_ptr(), m.t, m.rows, m.cols, eps,
+                          static_cast<dbf_mx_format>(fmt), data(m.h), static_cast<uint8_t*>(codes->data_ptr()),
+                          static_cast<uint8_t*>(scales->data_ptr()), stream()));
     PyObject* c = wrap(*codes);
     PyObject* s = wrap(*scales);
     PyObject* h = m.h ? wrap(*m.h) : (Py_INCREF(a[0]), a[0]);
@@ -295,9 +307,9 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     else dw = empty({m.cols}, at::kFloat, m.x);
     if (!work) work = empty({static_cast<int64_t>(p_backward_ws(m.rows, m.cols))}, at::kByte, m.x);
     check_status("dbf_rmsnorm_backward",
-                 p_norm_backward(dy.data_ptr(), m.x.data_ptr(), m.weight.data_ptr(), data(dh), m.t, m.rows, m.cols, eps,
-                                 dx->data_ptr(), static_cast<float*>(dw->data_ptr()), work->data_ptr(), work->nbytes(),
-                                 stream()));
+                 unlocked(p_norm_backward, dy.data_ptr(), m.x.data_ptr(), m.weight.data_ptr(), data(dh), m.t, m.rows,
+                          m.cols, eps, dx->data_ptr(), static_cast<float*>(dw->data_ptr()), work->data_ptr(),
+                          work->nbytes(), stream()));
     return pair(wrap(*dx), wrap(*dw));
   });
 }

@@ -424,3 +424,67 @@ def test_out_of_memory_is_torchs_error(dbf):
     with pytest.raises(torch.OutOfMemoryError):
         dbf.dbf_mx_forward(codes, scales, codes, scales, 1 << 20, 1, 1 << 20, x_fmt=mx.E2M1, w_fmt=mx.E2M1)
     dbf.dbf_mx_quantize(torch.zeros(2, 2, device="cuda"), mx.E2M1)
+
+
+def test_calls_release_the_interpreter(dbf):
+    """A launch may wait for room in the GPU's queue; other Python threads run meanwhile.  In place of the entry points
+    stands a function that answers whether its thread holds the interpreter's lock (as a status: 0, no)."""
+    import ctypes
+
+    binding, lib = dbf._binding(), dbf.load_library()
+    entries = [lib.dbf_mx_quantize, lib.dbf_mx_dequantize, lib.dbf_mx_forward, lib.dbf_rmsnorm_forward,
+               lib.dbf_rmsnorm_mx_forward, lib.dbf_rmsnorm_backward]
+    sizes = [lib.dbf_mx_code_bytes, lib.dbf_mx_scale_bytes, lib.dbf_mx_forward_workspace_bytes,
+             lib.dbf_rmsnorm_backward_workspace_bytes]
+    address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
+    x, w = torch.zeros(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    c, s = dbf.dbf_mx_quantize(x, mx.E4M3)
+    binding.init(dbf._raise_status, *[address(ctypes.pythonapi.PyGILState_Check)] * 6, *map(address, sizes))
+    try:
+        dbf.dbf_mx_quantize(x, mx.E4M3)
+        dbf.dbf_mx_dequantize(c, s, 4, 64, mx.E4M3)
+        dbf.dbf_mx_forward(c, s, c, s, 4, 64, 4, w_fmt=mx.E4M3)
+        dbf.dbf_rmsnorm_forward(x, w, 1e-5)
+        dbf.dbf_rmsnorm_mx_forward(x, w, 1e-5)
+        dbf.dbf_rmsnorm_backward(x, x, w, 1e-5)
+    finally:
+        binding.init(dbf._raise_status, *map(address, entries + sizes))
+
+
+def test_calls_from_two_threads(dbf):
+    """Two threads at once, each on its own stream, with a workspace between them: every result is the single call's."""
+    import threading
+
+    rng = np.random.default_rng(30)
+    sizes = [(1, 640, 900), (40, 640, 900), (300, 1000, 900)]
+    W = {n: held(rng.standard_normal((n, 900)), mx.E2M1) for _, n, _ in sizes}
+    X = {b: torch.from_numpy(rng.standard_normal((b, 900))).half().cuda() for b, _, _ in sizes}
+    g = torch.ones(900, dtype=torch.float16, device="cuda")
+    ws = dbf.dbf_mx_new_workspace(1000, 900, 300)
+
+    def run(b, n, m_in):
+        codes, scales, _ = dbf.dbf_rmsnorm_mx_forward(X[b], g, 1e-5, residual=X[b])
+        y = dbf.dbf_mx_forward(codes, scales, *W[n], n, m_in, b, workspace=ws, y_dtype=torch.float32)
+        return y, dbf.dbf_rmsnorm_backward(X[b], X[b], g, 1e-5)[1]
+
+    want = [run(*s) for s in sizes]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def thread():
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(60):
+                    got = [run(*s) for s in sizes]
+                    torch.cuda.current_stream().synchronize()
+                    if not all(torch.equal(a, b) for p, q in zip(got, want) for a, b in zip(p, q)):
+                        wrong.append("another result")
+        except Exception as e:  # noqa: BLE001
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=thread) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and dbf.dbf_workspace_status(ws) == 0
