@@ -600,7 +600,10 @@ def dbf_mx_forward(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch
                    n: int, m_in: int, batch: int, x_fmt: int = DBF_MX_E4M3, w_fmt: int = DBF_MX_E2M1,
                    y: Optional[torch.Tensor] = None, y_dtype: torch.dtype = torch.float16,
                    workspace: Optional[torch.Tensor] = None, flags: int = 0, stream=None) -> torch.Tensor:
-    """y = X W^T of two MX matrices, X batch x m_in and W n x m_in; returns y (batch x n)."""
+    """y = X W^T of two MX matrices, X batch x m_in and W n x m_in; returns y (batch x n).
+
+    A wait in the kernel that gave up shows in dbf_workspace_status(workspace): without a workspace the call makes one
+    of its own, whose status nobody can read."""
     return _on(stream, (_BINDING or _binding()).forward, x_codes, x_scales, w_codes, w_scales, n, m_in, batch, x_fmt,
                w_fmt, y, y_dtype, workspace, flags)
 

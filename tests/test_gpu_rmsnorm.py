@@ -329,3 +329,36 @@ def test_padding_behind_rows_with_nan(dbf, rows, cols, fmt):
         assert (byte[:, own:] == 0).all() and (code[:, cols:] == 0).all()
         bad = [1] if residual is None else [1, 4]
         assert (byte[bad, :own] == 255).all() and (byte[[0, 2, 5], :own] < 255).all()
+
+
+@pytest.mark.parametrize("batch", [1, 16, 130])
+def test_dense_norm_feeds_the_factorised_layer(dbf, batch):
+    """Residual and norm into a DBF layer's x and its result back into the residual stream, on one stream without a
+    synchronisation between, plain and replayed: the norm against its reference, the layer against the oracle on the
+    norm's own output (bars of test_gpu_parity)."""
+    import test_gpu_parity as parity
+
+    n, k, m_in = 512, 384, 768
+    layer = parity.random_layer(dbf, n, k, m_in, batch, seed=40)
+    ws = dbf.dbf_new_workspace(n, k, m_in, batch)
+    x, r, w = data(batch, m_in, "fp16", seed=41)
+    one = torch.ones(n, dtype=torch.float16, device="cuda")
+    z = torch.zeros(batch, n, dtype=torch.float16, device="cuda")
+
+    def run():
+        y, h = dbf.dbf_rmsnorm_forward(x, w, EPS, residual=r)
+        out = dbf.dbf_forward(y, layer.pA, layer.pB, layer.a, layer.mid, layer.b, n, k, m_in, workspace=ws)
+        return y, h, out, *dbf.dbf_rmsnorm_forward(out, one, EPS, residual=z)
+
+    plain = run()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        replayed = run()
+    g.replay()
+    for y, h, out, last, stream in (plain, replayed):
+        assert_dense(y, h, w, EPS, "fp16")
+        L = layer.np
+        want = parity.oracle.forward_staged(host(y), L["A"], L["B"], L["a"], L["mid"], L["b"])
+        parity.assert_fp16_close(host(out), want)
+        assert torch.equal(stream, out)
+        assert_dense(last, stream, one, EPS, "fp16")
