@@ -488,3 +488,49 @@ def test_calls_from_two_threads(dbf):
     for t in threads:
         t.join()
     assert not wrong and dbf.dbf_workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("fmt", [mx.E2M1, mx.E4M3])
+def test_quantize_at_the_largest_shapes(dbf, fmt):
+    """One row or column of 2^24: a long row equals the same blocks as many rows, a column its rows by themselves, and
+    the transposed forms each other."""
+    size = 1 << 24
+    g = torch.Generator(device="cuda").manual_seed(51)
+    v = torch.randn(size, generator=g, device="cuda").to(torch.bfloat16)
+    row, column, table = v.view(1, size), v.view(size, 1), v.view(size // 4096, 4096)
+    q = dbf.dbf_mx_quantize(row, fmt)
+    want = dbf.dbf_mx_dequantize(*dbf.dbf_mx_quantize(table, fmt), *table.shape, fmt)
+    assert torch.equal(dbf.dbf_mx_dequantize(*q, 1, size, fmt).view(-1), want.view(-1))
+    t = dbf.dbf_mx_quantize(column, fmt, transpose=True)
+    assert torch.equal(t[0], q[0])
+    assert torch.equal(dbf.dbf_mx_dequantize(*t, 1, size, fmt).view(-1), want.view(-1))
+    c = dbf.dbf_mx_quantize(column, fmt)
+    back = dbf.dbf_mx_dequantize(*c, size, 1, fmt).view(-1)
+    some = torch.cat([torch.arange(300, device="cuda"), torch.arange(size - 300, size, device="cuda")])
+    few = dbf.dbf_mx_dequantize(*dbf.dbf_mx_quantize(column[some].contiguous(), fmt), 600, 1, fmt).view(-1)
+    assert torch.equal(back[some], few)
+    t = dbf.dbf_mx_quantize(row, fmt, transpose=True)
+    assert torch.equal(t[0], c[0]) and torch.equal(dbf.dbf_mx_dequantize(*t, size, 1, fmt).view(-1), back)
+
+
+@pytest.mark.parametrize("xf,wf", [(mx.E2M1, mx.E2M1), (mx.E4M3, mx.E2M1)])
+@pytest.mark.parametrize("batch,n", [(1, 1 << 24), (70, 1 << 24), (1 << 24, 3), (1 << 24, 300)])
+def test_product_at_the_largest_shapes(dbf, batch, n, xf, wf):
+    """2^24 weight rows or tokens: whole numbers, exact at both ends and at random places between."""
+    m_in = 33
+    g = torch.Generator(device="cuda").manual_seed(52)
+    pick = lambda rows: torch.tensor([0.0, 1, 2, 3, -1, -2, -6], device="cuda")[  # noqa: E731
+        torch.randint(0, 7, (rows, m_in), generator=g, device="cuda")].to(torch.bfloat16)
+    X, W = pick(batch), pick(n)
+    y = dbf.dbf_mx_forward(*dbf.dbf_mx_quantize(X, xf), *dbf.dbf_mx_quantize(W, wf), n, m_in, batch, x_fmt=xf, w_fmt=wf,
+                           y_dtype=torch.float32 if n < 300 or batch == 1 else torch.float16)
+    X, W = (dbf.dbf_mx_dequantize(*dbf.dbf_mx_quantize(t, f), t.shape[0], m_in, f) for t, f in ((X, xf), (W, wf)))
+
+    def some(size):
+        if size < 1000:
+            return torch.arange(size, device="cuda")
+        return torch.cat([torch.arange(300, device="cuda"), torch.arange(size - 300, size, device="cuda"),
+                          torch.randint(0, size, (1000,), generator=g, device="cuda")])
+
+    i, j = some(batch), some(n)
+    assert torch.equal(y[i][:, j].double(), X[i].double() @ W[j].double().t())

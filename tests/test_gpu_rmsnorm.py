@@ -362,3 +362,43 @@ def test_dense_norm_feeds_the_factorised_layer(dbf, batch):
         parity.assert_fp16_close(host(out), want)
         assert torch.equal(stream, out)
         assert_dense(last, stream, one, EPS, "fp16")
+
+
+@pytest.mark.parametrize("alias", ["dh", "dy"])
+@pytest.mark.parametrize("rows,cols", GRAD_FORMS)
+def test_backward_in_place_in_every_form(dbf, rows, cols, alias):
+    for kind in ("bf16", "fp32"):
+        h, dy, w = data(rows, cols, kind, seed=2)
+        dh = data(rows, cols, kind, seed=3)[0]
+        want = dbf.dbf_rmsnorm_backward(dy, h, w, EPS, dh=dh)
+        dx, dw = dbf.dbf_rmsnorm_backward(dy, h, w, EPS, dh=dh, dx=dh if alias == "dh" else dy)
+        assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+
+
+@pytest.mark.parametrize("rows,cols", [(1 << 24, 1), (2, 1 << 20), (1, (1 << 20) - 1)])
+def test_largest_shapes(dbf, rows, cols):
+    """The ends of the shape contract against the formulas in fp64 on the GPU (tolerances as above; a row that fits no
+    block adds cols / 1024 squares a thread, which rel() counts)."""
+    g = torch.Generator(device="cuda").manual_seed(50)
+    h, dy = (torch.randn(rows, cols, generator=g, device="cuda") for _ in range(2))
+    w = 1 + 0.2 * torch.randn(cols, generator=g, device="cuda")
+    H, D, W = h.double(), dy.double(), w.double()
+    r = 1 / torch.sqrt((H * H).mean(1, keepdim=True) + EPS)
+    d = rel(cols)
+    y, _ = dbf.dbf_rmsnorm_forward(h, w, EPS)
+    assert ((y - H * r * W).abs() <= (d + U * (1 + d)) * (H * r * W).abs() + TINY["fp32"]).all()
+    codes, scales, _ = dbf.dbf_rmsnorm_mx_forward(h, w, EPS, mx.E4M3)
+    back = dbf.dbf_mx_dequantize(codes, scales, rows, cols, mx.E4M3)
+    # e4m3: off by 2^-4 of the value, by (512 - 448) / 512 = 2^-3 where a block's largest saturates, and by half of the
+    # smallest step, 2^-10 of a scale of 2^-8 of the top at most
+    top = (H * r * W).abs()
+    top = top if cols == 1 else torch.nn.functional.pad(top, (0, -cols % 32)).view(rows, -1, 32).amax(2).repeat_interleave(
+        32, 1)[:, :cols]
+    assert ((back - H * r * W).abs() <= (1 + 2 * d) * (2.0 ** -3 * (H * r * W).abs() + 2.0 ** -18 * top)).all()
+    dx, dw = dbf.dbf_rmsnorm_backward(dy, h, w, EPS)
+    size = r * (D * W).abs() + r * (H * r).abs() * (D * W * H * r).abs().mean(1, keepdim=True)
+    m = (D * W * H * r).mean(1, keepdim=True)
+    assert ((dx - (r * D * W - r * H * r * m)).abs() <= 2 * 4 * d * size + 2 * U * size + TINY["fp32"]).all()
+    # 2^24 rows: a warp adds 2^24 / (8 * 296) of them one after another, then eight and 296 sums
+    assert ((dw - (D * H * r).sum(0)).abs() <= (rows / 2368 + 320 + 1) * U * (D * H * r).abs().sum(0) * (1 + 4 * d) + 4 * d * (
+        D * H * r).abs().sum(0)).all()
