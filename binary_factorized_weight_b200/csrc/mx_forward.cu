@@ -64,8 +64,10 @@ __device__ __forceinline__ void store_out(void* out, int t, int64_t at, float v)
 // 250 cycles of waiting and signalling however little it multiplies (one token x
 // 14336 x 4096, 8-bit tokens: 9.5 us with one step, 9.1 with two).
 // Measured: 4-bit weights of 4096 x 4096 / 14336 x 4096, one token in 8 bits 4.6 /
-// 9.1 us (the weights' DRAM time is 30 / 53% of that), in 4 bits 7.7 us for the wide
-// one; 16 tokens 5.1 / 9.5 us; 128 tokens x 4096 x 4096 8.6 us.
+// 9.0 us (the weights' DRAM time is 30 / 53% of that), in 4 bits 7.7 us for the wide
+// one; 16 tokens 5.1 / 9.4 us; 128 tokens x 4096 x 4096 8.6 us.  The wide layer's 112
+// tiles cannot be split by two over 148 SMs: 36 of them have no work, and the
+// others read a whole row of tiles each.
 template <int KA, int NT>
 struct SplitCfg {
   static constexpr int U = NT <= 32 ? 2 : 1;
@@ -328,7 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // costs it 32 KB where a CTA alone would fetch 48; the MMA reads both.  The
 // pairs are persistent (one CTA per SM) and walk the work items, tokens fastest;
 // the ring runs on across items.  Tiles that would leave most pairs idle (all of
-// few, or the last round's) are cut into 2 or 4 items of 128 or 64 weight rows.
+// few, or the last round's) are cut into 2 or 4 items of 128 or 64 weight rows (which
+// still fetch a whole tile's weight rows: a step of a quarter costs 0.25 us where a
+// whole one costs 0.34).  Up to 128 tokens the odd CTA of a pair multiplies only
+// rows behind the last token.
 // Accumulators: tensor memory holds two of 256 columns that overlap in their
 // last / first columns (both do not fit beside the scales), so the MMAs of an
 // item wait only until the epilogue has read the shared columns of the one before.
@@ -889,11 +894,15 @@ dbf_status launch_mx(const Operand& x, const Operand& w, const MxArgs& base, int
   MxArgs a = base;
   a.steps_k = static_cast<int>((a.k4s + KA - 1) / KA);
   if (x.rows > 64) {
-    // Estimated microseconds of both kernels, from times measured at 1024 and
-    // 4096 x 4096, 14336 x 4096, 4096 x 14336 and 4096 x 512 for 32 to 2048
-    // tokens: a step of K costs a CTA of the split kernel 0.44 (4-bit operands,
-    // twice the K: 0.62), a pair 0.34 / 0.27 / 0.25 for 256 / 128 / 64 weight
-    // rows (4-bit: 0.39 / 0.32 / 0.30).
+    // Estimated microseconds of both kernels: a step of K costs a CTA of the split
+    // kernel 0.44 (4-bit operands, twice the K: 0.62), a pair 0.34 / 0.27 / 0.25
+    // for 256 / 128 / 64 weight rows (4-bit: 0.39 / 0.32 / 0.30).  Both kernels timed
+    // for 65 to 1024 tokens in both formats at 1024, 4096 and 14336 x 4096 and
+    // 4096 x 14336 (56 points): the pairs take 0.89 to 1.29 of their estimate, the
+    // split kernel 0.56 to 1.00, and the choice is the faster one or within 2.2% of
+    // it at 49.  It loses 26 / 19% (4- / 8-bit tokens) for 65 tokens and 8 / 5% for
+    // 128 at 14336 x 4096 (13.6 us on pairs, 10.8 split), 18% for 192 and 256 tokens
+    // at 4096 x 14336 in 4 bits, 7% for 192 at 4096 x 4096 in 8.
     const bool four = KA == 2;
     const int64_t split_tiles = (w.rows + kRows - 1) / kRows * ((x.rows + 127) / 128);
     const int ks = split_ways(split_tiles, a.steps_k, dev.num_sms);

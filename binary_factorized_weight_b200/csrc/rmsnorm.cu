@@ -57,8 +57,9 @@ constexpr int kStagedThreads = 512;   // threads of a block that stages its rows
 // A row is the work of one warp (WARP: up to 1024 columns, eight rows to a
 // block) or of a block; persistent over rows.  Thread t of the row owns the
 // sixteen columns of chunks t, t + threads, .. (NV of them, held in registers,
-// so everything is read once).  NV = 0: any number of chunks, the second pass
-// reads h (or x) again.
+// so everything is read once; of two chunks in aligned blocks of up to 1024 threads,
+// 16385 to 32768 columns, 128 bytes a thread in 16 bits and some 500 in fp32
+// are spilled).  NV = 0: any number of chunks, the second pass reads h (or x) again.
 template <typename T, int OUT, int NV, bool VEC, bool WARP>
 __global__ void __launch_bounds__(VEC && !WARP ? 1024 : kStagedThreads) dbf_rmsnorm_kernel(const NormArgs p) {
   __shared__ float red[2][32];
@@ -246,7 +247,8 @@ __device__ __forceinline__ void row_sums(float (&v)[M], float* red) {
 // block an eighth of the columns, so that no second launch is needed.
 // VEC: a thread owns sixteen neighbouring columns (32-byte accesses); else every
 // 32nd of its warp's 512 columns.  PRE: the next row is loaded while this one is reduced (16-
-// bit elements: more does not fit the registers).
+// bit elements: more does not fit the registers; the unaligned forms spill 32 to 48
+// bytes of it).
 constexpr int kGradThreads = 512;
 constexpr int kFewBlocks = 8;  // SPAN 3: the blocks of the cluster
 template <typename T, bool VEC, int SPAN>
@@ -521,7 +523,9 @@ dbf_status launch_grad_sum(const NormGradArgs& a, cudaStream_t stream) {
 }
 
 // How the rows are shared out, from the sizes alone (the workspace's size and
-// dweight's order of additions follow from it).
+// dweight's order of additions follow from it).  Clusters are counted by the SMs, not
+// by how many are resident together: of eight blocks fewer than 18 may be, and the
+// rest then run behind them.
 constexpr int kGradSms = 148;
 constexpr int64_t kFewRows = 16;
 struct GradPlan {
