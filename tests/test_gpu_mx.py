@@ -534,3 +534,33 @@ def test_product_at_the_largest_shapes(dbf, batch, n, xf, wf):
 
     i, j = some(batch), some(n)
     assert torch.equal(y[i][:, j].double(), X[i].double() @ W[j].double().t())
+
+
+@pytest.mark.parametrize("batch", [1, 20, 100, 300])
+@pytest.mark.parametrize("xf,wf", FORMATS)
+def test_what_lay_in_the_buffers_reaches_no_result(dbf, batch, xf, wf):
+    """Codes and scales written into buffers of 0xFF (NaN scales, which rows behind the last one keep): the matrices and
+    their product are those of fresh buffers, bit for bit, from the quantisation, its transpose and the norm."""
+    n, m_in = 333, 200
+    g = torch.Generator(device="cuda").manual_seed(60)
+    X, W = torch.randn(batch, m_in, generator=g, device="cuda"), torch.randn(n, m_in, generator=g, device="cuda")
+    weight = torch.ones(m_in, device="cuda")
+
+    def used(rows, fmt):
+        full = lambda size: torch.full((size,), 255, dtype=torch.uint8, device="cuda")  # noqa: E731
+        return dict(codes=full(dbf.dbf_mx_code_bytes(rows, m_in, fmt)), scales=full(dbf.dbf_mx_scale_bytes(rows, m_in)))
+
+    kw = dict(x_fmt=xf, w_fmt=wf, y_dtype=torch.float32)
+    w = dbf.dbf_mx_quantize(W, wf)
+    want = dbf.dbf_mx_forward(*dbf.dbf_mx_quantize(X, xf), *w, n, m_in, batch, **kw)
+    assert torch.isfinite(want).all()
+    dirty = dbf.dbf_mx_quantize(X.t().contiguous(), xf, transpose=True, **used(batch, xf))
+    for other in (dbf.dbf_mx_quantize(W, wf, **used(n, wf)),
+                  dbf.dbf_mx_quantize(W.t().contiguous(), wf, transpose=True, **used(n, wf))):
+        assert torch.equal(other[0], w[0])
+        assert torch.equal(dbf.dbf_mx_forward(*dirty, *other, n, m_in, batch, **kw), want)
+    clean = dbf.dbf_rmsnorm_mx_forward(X, weight, 1e-5, xf)
+    normed = dbf.dbf_rmsnorm_mx_forward(X, weight, 1e-5, xf, **used(batch, xf))
+    assert torch.equal(normed[0], clean[0])
+    assert torch.equal(dbf.dbf_mx_forward(*normed[:2], *w, n, m_in, batch, **kw),
+                       dbf.dbf_mx_forward(*clean[:2], *w, n, m_in, batch, **kw))
